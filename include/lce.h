@@ -231,6 +231,115 @@ lce_status_t lce_forward_static_scratch(const void* H, const void* W, const int6
                                         int64_t* n_valid, uint32_t* device_error_flags,
                                         void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The feed-forward block in front of the vocabulary projection, and the clipping of the
+ * gradients behind it.
+ *
+ * Conventions of the entry points below, beyond those at the top of this file
+ *   - dtype is LCE_BF16 (bf16 arrays, fp32 accumulation) or LCE_F32 (fp32 arrays, products and
+ *     sums accurate to fp32); every array of a call, gradients included, has that type.  Sums and
+ *     the activation are fp32; each result is rounded once.
+ *   - Weights, biases and weight gradients are dense; X, residual, Y and dY have row strides
+ *     (elements) at least their width, so slices of wider arrays can be passed.
+ *   - Shape rules (LCE_ERR_UNSUPPORTED_SHAPE otherwise): N >= 0 (N = 0: nothing is written but
+ *     zero weight gradients), widths >= 1 whose rows are multiples of 16 bytes (multiples of 8 for
+ *     LCE_BF16, of 4 for LCE_F32), row strides likewise; all < 2^31.  Every pointer is 16-byte
+ *     aligned; outputs do not overlap inputs, except Y == residual with equal strides.
+ *   - The workspace is at least the size its function names; nothing in it is kept between calls.
+ *     lce_check_error on it reports a wait that timed out.
+ *   - Outputs are bitwise reproducible for a fixed device and fixed shapes.  A row of Y or H does
+ *     not depend on the other rows' values, but its summation order may differ between the call
+ *     for a few tokens and the call for many.
+ *   - An inf or NaN in an operand makes the outputs it takes part in inf or NaN.  With LCE_F32 an
+ *     inf may come out as NaN: operands are summed in parts.
+ */
+typedef enum {
+  LCE_ACT_NONE = 0,
+  LCE_ACT_RELU = 1,
+  LCE_ACT_SILU = 2,      /* x / (1 + e^-x)                                  */
+  LCE_ACT_GELU = 3,      /* x Phi(x), by the error function                 */
+  LCE_ACT_GELU_TANH = 4  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+} lce_activation_t;
+
+/* Workspace bytes of the linear entry points (backward: 0 or 1); 0 on a broken shape rule. */
+size_t lce_linear_workspace_size(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t activation,
+                                 int32_t backward, lce_dtype_t dtype);
+
+/*
+ * Y [N x d_out] = act(X W^T + b) + R for X [N x d_in], W [d_out x d_in], bias b [d_out] and
+ * residual R [N x d_out]; bias and residual may be NULL.
+ */
+lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const void* bias,
+                                const void* residual, int64_t ldr, int64_t N, int64_t d_in,
+                                int64_t d_out, lce_activation_t activation, lce_dtype_t dtype,
+                                void* Y, int64_t ldy, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * Gradients of lce_linear_forward from the outgoing gradient dY [N x d_out]:
+ *   dZ = dY * act'(X W^T + b),  dX = dZ W,  dW = dZ^T X,  dbias = column sums of dZ
+ * (the residual's gradient is dY).  The pre-activations are recomputed, not kept from the forward
+ * pass; with LCE_ACT_NONE there is nothing to recompute and bias is not read.  dX [N x d_in], dW
+ * [d_out x d_in] and dbias [d_out] are dense; a gradient whose pointer is NULL is not computed.
+ * For LCE_BF16 dZ is rounded to bf16 as an operand of the products.
+ */
+lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, const void* bias,
+                                 const void* dY, int64_t ldy, int64_t N, int64_t d_in,
+                                 int64_t d_out, lce_activation_t activation, lce_dtype_t dtype,
+                                 void* dX, void* dW, void* dbias, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the gated entry points (backward: 0 or 1); 0 on a broken shape rule. */
+size_t lce_gated_workspace_size(int64_t N, int64_t d, int64_t F, int32_t backward,
+                                lce_dtype_t dtype);
+
+/*
+ * H [N x F] = act(X Wg^T) * (X Wu^T) for X [N x d], Wg and Wu [F x d], in one kernel: neither
+ * projection is stored.
+ */
+lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t N,
+                               int64_t d, int64_t F, lce_activation_t activation,
+                               lce_dtype_t dtype, void* H, int64_t ldh, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of lce_gated_forward from the outgoing gradient dH [N x F].  With G = X Wg^T and
+ * U = X Wu^T (recomputed, not kept from the forward pass):
+ *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
+ * dX [N x d], dWg and dWu [F x d] are dense; dX, or dWg and dWu together, may be NULL and are then
+ * not computed.  For LCE_BF16 dG and dU are rounded to bf16 as operands of the products.
+ */
+lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, const void* Wu,
+                                const void* dH, int64_t ldh, int64_t N, int64_t d, int64_t F,
+                                lce_activation_t activation, lce_dtype_t dtype, void* dX, void* dWg,
+                                void* dWu, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Global norm of `count` gradient arrays, and their scaling.  grads, out, numels and dtypes are
+ * HOST arrays of `count` entries that are read during the call: device pointers, element counts
+ * (0 allowed, the pointer may then be NULL) and types (LCE_BF16 or LCE_F32, mixed freely).  The
+ * device arrays are dense and aligned to their element size; 16-byte alignment is not needed.
+ *   LCE_NORM_L2   total = sqrt(sum of g^2): squares in fp32, summed per thread over at most 64
+ *                 values in fp32 and beyond that in fp64; squares that pass fp32 (|g| > 1.8e19)
+ *                 count as inf
+ *   LCE_NORM_INF  total = max |g|
+ * A NaN anywhere gives a NaN total.  total_norm is a device fp32 scalar.
+ * lce_clip_grad_norm then writes out[i] = grads[i] * c, c = min(1, max_norm / (total + 1e-6)) in
+ * fp32, rounded once; out[i] may be grads[i] (out == NULL: all in place), any other overlap of an
+ * output with an input or output is not allowed.  In place with c = 1 nothing is written.  A NaN
+ * total makes every output NaN, an infinite one makes c = 0.
+ * The order of every sum is fixed by the counts and the device: results are reproducible.
+ */
+typedef enum { LCE_NORM_L2 = 0, LCE_NORM_INF = 1 } lce_norm_t;
+size_t lce_grad_norm_workspace_size(int64_t count);
+lce_status_t lce_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
+                           int64_t count, lce_norm_t norm, float* total_norm, void* workspace,
+                           size_t ws_bytes, void* stream);
+lce_status_t lce_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numels,
+                                const int32_t* dtypes, int64_t count, lce_norm_t norm,
+                                float max_norm, float* total_norm, void* workspace,
+                                size_t ws_bytes, void* stream);
+
 /*
  * Synchronises stream, then reads the workspace error flags written by the device:
  * LCE_ERR_TIMEOUT, else LCE_ERR_LABEL_OUT_OF_RANGE, else LCE_OK (LCE_ERR_CUDA if the copy or the
@@ -291,7 +400,10 @@ int32_t lce_trace_end(void);
  * "tc_bwd_grad" (a strip's gradient), "tc_dh_dw" (a strip's dH and / or dW), "tc_bwd" (dH and dW
  * of one strip with the gradient of the next, for small backward steps); CUDA-core launches of
  * the exact fp32 path: "simt_fwd_lse", "simt_bwd_grad", "simt_dh", "simt_dw"; and "combine",
- * "finalize", "split_tf32".
+ * "finalize", "split_tf32".  Feed-forward operators: "linear", "linear_dz", "gated",
+ * "gated_dg_du" (the gradients of the pre-activations), "ffn_grads" (dX and / or the weight
+ * gradients), "column_sum" (dbias), "split_bf16" (fp32 operands into bf16 parts).  Clipping:
+ * "grad_norm", "grad_scale".
  */
 const char* lce_kernel_name(int32_t kernel_id);
 

@@ -20,7 +20,10 @@ def __getattr__(name):
     # torch.cuda; it never falls back to anything when the library is missing.
     if name in ("lce_workspace_size", "lce_strip_columns", "lce_forward", "lce_backward", "lce_check_error",
                 "lce_host_buffer_size", "lce_forward_backward_host", "lce_launch_count",
-                "linear_cross_entropy", "LinearCrossEntropy"):
+                "linear_cross_entropy", "LinearCrossEntropy", "lce_linear_workspace_size",
+                "lce_linear_forward", "lce_linear_backward", "lce_gated_workspace_size",
+                "lce_gated_forward", "lce_gated_backward", "lce_grad_norm", "lce_clip_grad_norm",
+                "linear_act", "gated_linear", "clip_grad_norm_", "LinearAct", "GatedLinear"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

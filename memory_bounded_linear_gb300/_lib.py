@@ -21,6 +21,8 @@ STATUS_NAMES = {
 REDUCTIONS = {"mean": 0, "sum": 1}
 DTYPES = {"bf16": 0, "f32": 1, "tf32x3": 2}
 GRAD_PARTS = {"dh": 1, "dw": 2, "both": 3}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+NORMS = {"l2": 0, "inf": 1}
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
@@ -45,6 +47,27 @@ _SIGNATURES = {
                                                  _c_i64, _c_i64, ctypes.c_int, ctypes.c_int, _c_p,
                                                  _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                                  ctypes.c_size_t, _c_p, _c_p, _c_p]),
+    "lce_linear_workspace_size": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, ctypes.c_int,
+                                                    ctypes.c_int32, ctypes.c_int]),
+    "lce_linear_forward": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                          _c_i64, ctypes.c_int, ctypes.c_int, _c_p, _c_i64, _c_p,
+                                          ctypes.c_size_t, _c_p]),
+    "lce_linear_backward": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                           _c_i64, ctypes.c_int, ctypes.c_int, _c_p, _c_p, _c_p,
+                                           _c_p, ctypes.c_size_t, _c_p]),
+    "lce_gated_workspace_size": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, ctypes.c_int32,
+                                                   ctypes.c_int]),
+    "lce_gated_forward": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                         ctypes.c_int, ctypes.c_int, _c_p, _c_i64, _c_p,
+                                         ctypes.c_size_t, _c_p]),
+    "lce_gated_backward": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                          _c_i64, ctypes.c_int, ctypes.c_int, _c_p, _c_p, _c_p,
+                                          _c_p, ctypes.c_size_t, _c_p]),
+    "lce_grad_norm_workspace_size": (ctypes.c_size_t, [_c_i64]),
+    "lce_grad_norm": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i64, ctypes.c_int, _c_p, _c_p,
+                                     ctypes.c_size_t, _c_p]),
+    "lce_clip_grad_norm": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_int,
+                                          ctypes.c_float, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "lce_check_error": (ctypes.c_int, [_c_p, _c_p]),
     "lce_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "lce_last_cuda_error": (ctypes.c_char_p, []),

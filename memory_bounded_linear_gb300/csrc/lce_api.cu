@@ -203,31 +203,6 @@ struct Trace {
 };
 Trace g_trace;
 
-template <typename F>
-cudaError_t traced(int kid, cudaStream_t stream, F&& launch) {
-  const bool rec = g_trace.active && g_trace.n < g_trace.cap;
-  if (rec) {
-    cudaError_t e = cudaEventRecord(static_cast<cudaEvent_t>(g_trace.start[g_trace.n]), stream);
-    if (e != cudaSuccess) return e;
-  }
-  // Drop a stale, non-sticky error another library may have left on this thread, so that the
-  // check after the launch reports only this launch (sticky errors are reported again anyway).
-  (void)cudaGetLastError();
-  g_detail_set = false;
-  g_extra_kernels = 0;
-  cudaError_t e = note(launch());
-  if (e != cudaSuccess) return e;
-  g_launches.fetch_add(1 + g_extra_kernels, std::memory_order_relaxed);
-  g_extra_kernels = 0;
-  if (rec) {
-    e = cudaEventRecord(static_cast<cudaEvent_t>(g_trace.stop[g_trace.n]), stream);
-    if (e != cudaSuccess) return e;
-    g_trace.ids[g_trace.n] = kid;
-    ++g_trace.n;
-  }
-  return cudaSuccess;
-}
-
 cudaError_t strip_gemm(const StripArgs& a, lce_dtype_t dt, cudaStream_t stream, int num_sms) {
   if (dt != LCE_F32)  // the tensor-core backward goes through tc_strip_jobs, never through here
     return traced(K_TC_FWD, stream, [&] { return tc_strip_gemm(a, stream, num_sms); });
@@ -284,6 +259,32 @@ void set_x3_operands(StripArgs& a, char* ws, const Layout& L) {
 }  // namespace
 
 thread_local int g_extra_kernels = 0;
+
+cudaError_t launch_open(cudaStream_t stream, bool* rec) {
+  *rec = g_trace.active && g_trace.n < g_trace.cap;
+  if (*rec) {
+    cudaError_t e = cudaEventRecord(static_cast<cudaEvent_t>(g_trace.start[g_trace.n]), stream);
+    if (e != cudaSuccess) return e;
+  }
+  // Drop a stale, non-sticky error another library may have left on this thread, so that the
+  // check after the launch reports only this launch (sticky errors are reported again anyway).
+  (void)cudaGetLastError();
+  g_detail_set = false;
+  g_extra_kernels = 0;
+  return cudaSuccess;
+}
+
+cudaError_t launch_close(int kid, cudaStream_t stream, bool rec) {
+  g_launches.fetch_add(1 + g_extra_kernels, std::memory_order_relaxed);
+  g_extra_kernels = 0;
+  if (rec) {
+    cudaError_t e = cudaEventRecord(static_cast<cudaEvent_t>(g_trace.stop[g_trace.n]), stream);
+    if (e != cudaSuccess) return e;
+    g_trace.ids[g_trace.n] = kid;
+    ++g_trace.n;
+  }
+  return cudaSuccess;
+}
 
 void set_error_detail(const char* fmt, ...) {
   va_list ap;
@@ -682,7 +683,10 @@ const char* lce_kernel_name(int32_t id) {
   static const char* names[K_NUM] = {"tc_fwd_lse",    "tc_bwd",   "simt_fwd_lse",
                                      "simt_bwd_grad", "simt_dh",  "simt_dw",
                                      "combine",       "finalize", "split_tf32",
-                                     "tc_bwd_grad",   "tc_dh_dw"};
+                                     "tc_bwd_grad",   "tc_dh_dw", "linear",
+                                     "linear_dz",     "gated",    "gated_dg_du",
+                                     "ffn_grads",     "column_sum", "grad_norm",
+                                     "grad_scale",    "split_bf16"};
   return (id >= 0 && id < K_NUM) ? names[id] : nullptr;
 }
 

@@ -41,10 +41,15 @@ enum Mode : int {
 // K_TC_BWD is an overlapped backward step: dH and dW of one strip together with the gradient of
 // the next.  K_TC_GRAD is a strip's gradient alone; K_TC_DHDW its dH and / or dW.
 // K_SPLIT is the tf32 hi / lo split of an fp32 operand (plain or transposed).
+// The feed-forward operators: K_LIN and K_GATED forward, K_LIN_DZ and K_GATED_DGU the gradients of
+// their pre-activations, K_FFN_GRADS dX and / or dW, K_COLSUM dbias, K_SPLIT_BF16 the split of an
+// fp32 operand into bf16 parts.  K_GRAD_NORM and K_GRAD_SCALE are the two passes of clipping.
 enum KernelId : int {
   K_TC_FWD = 0, K_TC_BWD = 1,
   K_SIMT_FWD = 2, K_SIMT_BWD_G = 3, K_SIMT_DH = 4, K_SIMT_DW = 5,
-  K_COMBINE = 6, K_FINALIZE = 7, K_SPLIT = 8, K_TC_GRAD = 9, K_TC_DHDW = 10, K_NUM = 11
+  K_COMBINE = 6, K_FINALIZE = 7, K_SPLIT = 8, K_TC_GRAD = 9, K_TC_DHDW = 10,
+  K_LIN = 11, K_LIN_DZ = 12, K_GATED = 13, K_GATED_DGU = 14, K_FFN_GRADS = 15, K_COLSUM = 16,
+  K_GRAD_NORM = 17, K_GRAD_SCALE = 18, K_SPLIT_BF16 = 19, K_NUM = 20
 };
 
 // Operand formats of the tensor-core engine.  OP_BF16: bf16 operands.  OP_TF32X3: fp32 operands
@@ -90,6 +95,19 @@ struct StripArgs {
 
 // Kernels a launcher started beyond its first one (the launch counter adds them), per thread.
 extern thread_local int g_extra_kernels;
+
+// Launch bookkeeping (lce_api.cu): trace events around a launch and the launch counter.
+cudaError_t launch_open(cudaStream_t stream, bool* rec);
+cudaError_t launch_close(int kid, cudaStream_t stream, bool rec);
+template <typename F>
+cudaError_t traced(int kid, cudaStream_t stream, F&& launch) {
+  bool rec = false;
+  cudaError_t e = launch_open(stream, &rec);
+  if (e != cudaSuccess) return e;
+  e = note(launch());
+  if (e != cudaSuccess) return e;
+  return launch_close(kid, stream, rec);
+}
 
 // Records a human-readable description of the last failure on the calling thread (reported by
 // lce_last_cuda_error).  printf-style.

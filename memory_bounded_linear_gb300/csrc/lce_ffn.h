@@ -35,10 +35,42 @@ struct FfnGemm {
   void* C2;                        // FFN_GATED_DGU (row stride ldc)
 };
 
+// An operand of the tensor-core kernel as it is stored: bf16 rows of stored_cols elements, ld
+// elements apart; for fp32 three such arrays (the bf16 parts), part_stride elements apart.
+struct FfnOperand {
+  const void* ptr;
+  int64_t stored_rows, stored_cols, ld;
+  int64_t parts, part_stride;
+};
+
+// One product for the tensor-core kernel; fields as in FfnGemm.  a_mn / b_mn: stored [K x rows].
+// For LCE_F32 the pre-activation gradients C and C2 are written as bf16 parts (row stride ldc,
+// part_stride apart), and C of the other modes as fp32.
+struct FfnTc {
+  int mode;
+  lce_activation_t act;
+  int64_t M, Ncols, K;
+  FfnOperand A, B, A2, B2;
+  bool a_mn, b_mn;
+  const void* bias;
+  const void* R; int64_t ldr;
+  const void* D; int64_t ldd;
+  void* C; int64_t ldc;
+  void* C2;
+  int64_t part_stride;
+};
+
+// Tensor cores: lce_ffn_tc.cu.  Several jobs only for FFN_GRADS; header: the workspace header.
+cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
+                          int num_sms, cudaStream_t stream);
+// fp32 x [rows x cols], row stride ld, into three bf16 parts of row stride ld_out: lce_ffn_simt.cu
+cudaError_t launch_split_bf16(const float* x, int64_t ld, int64_t rows, int64_t cols, void* out,
+                              int64_t ld_out, int64_t part_stride, cudaStream_t stream);
 // CUDA cores, any mode, type and layout: lce_ffn_simt.cu
 cudaError_t launch_ffn_simt(const FfnGemm& g, cudaStream_t stream);
-// out[c] = sum over the N rows of x[., c], row stride ld: lce_ffn_simt.cu
+// out[c] = sum over the N rows of x[., c], row stride ld; parts = 3: x holds three bf16 parts,
+// part_stride apart, and out is fp32: lce_ffn_simt.cu
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, lce_dtype_t dtype,
-                              void* out, cudaStream_t stream);
+                              int parts, int64_t part_stride, void* out, cudaStream_t stream);
 
 }  // namespace lce

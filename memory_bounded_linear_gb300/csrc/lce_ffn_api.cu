@@ -27,57 +27,120 @@ bool width_ok(int64_t w, lce_dtype_t dt) {
 }
 bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
 
-// Workspace: header (error flags), then the gradients of the pre-activations [N x width] each.
+// Products of at most this many tokens (forward) run on the CUDA-core kernel, larger ones on the
+// tensor cores, whose tiles hold 256 tokens.
+constexpr int64_t kFewTokens = 128;
+
+int64_t round8(int64_t x) { return (x + 7) & ~int64_t(7); }
+
+// One array of the workspace.  LCE_BF16: [rows x cols] bf16.  LCE_F32: three bf16 parts of it, rows
+// padded to 16 bytes.
+struct Slot {
+  size_t off;
+  int64_t ld, part_stride;
+};
+
+// Workspace: header (error flags, scheduler counters), then for LCE_F32 the parts of X and of the
+// weights (products on the tensor cores), then the gradients of the pre-activations.
 struct Layout {
-  size_t off_z[2];
+  Slot x, w[2], z[2];
   size_t total;
 };
 
-Layout layout(int64_t N, int64_t width, int nz, lce_dtype_t dt) {
+Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool backward,
+              lce_dtype_t dt) {
   Layout L{};
   size_t off = WS_HEADER_BYTES;
-  for (int i = 0; i < nz; ++i) {
-    L.off_z[i] = off;
-    off += align256(static_cast<size_t>(N) * static_cast<size_t>(width) * elem(dt));
+  auto take = [&](Slot& s, int64_t rows, int64_t cols) {
+    s.off = off;
+    s.ld = dt == LCE_BF16 ? cols : round8(cols);
+    s.part_stride = rows * s.ld;
+    off += align256(static_cast<size_t>(s.part_stride) * 2 * (dt == LCE_BF16 ? 1 : 3));
+  };
+  if (dt == LCE_F32 && (backward || N > kFewTokens)) {
+    take(L.x, N, d);
+    for (int i = 0; i < weights; ++i) take(L.w[i], width, d);
   }
+  for (int i = 0; i < nz; ++i) take(L.z[i], N, width);
   L.total = off;
   return L;
 }
 
-cudaError_t gemm(int kid, const FfnGemm& g, cudaStream_t stream) {
-  if (g.M == 0) return cudaSuccess;
-  return traced(kid, stream, [&] { return launch_ffn_simt(g, stream); });
+Layout linear_layout(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t act, bool backward,
+                     lce_dtype_t dt) {
+  // with no activation dZ is dY: read in place, or (fp32) split into parts
+  const int nz = backward && (act != LCE_ACT_NONE || dt == LCE_F32) ? 1 : 0;
+  return layout(N, d_in, d_out, 1, nz, backward, dt);
+}
+Layout gated_layout(int64_t N, int64_t d, int64_t F, bool backward, lce_dtype_t dt) {
+  return layout(N, d, F, 2, backward ? 2 : 0, backward, dt);
 }
 
 cudaError_t zero(void* p, size_t bytes, cudaStream_t stream) {
   return (p && bytes) ? note(cudaMemsetAsync(p, 0, bytes, stream)) : cudaSuccess;
 }
 
-// dX = dZ W (+ dZ2 W2) and dW = dZ^T X (and dW2 = dZ2^T X) for dZ [N x width] with row stride ldz.
-lce_status_t products(const void* X, int64_t ldx, const void* W, const void* W2, const void* dZ,
-                      const void* dZ2, int64_t ldz, int64_t N, int64_t d, int64_t width,
-                      lce_dtype_t dt, void* dX, void* dW, void* dW2, cudaStream_t stream) {
-  FfnGemm g{};
-  g.mode = FFN_GRADS;
-  g.dtype = dt;
-  g.act = LCE_ACT_NONE;
-  for (int i = 0; i < (dW2 ? 2 : 1); ++i) {
-    if (!dW) break;
-    g.M = width; g.Ncols = d; g.K = N;
-    g.A = i ? dZ2 : dZ; g.lda = ldz; g.a_t = true;
-    g.B = X; g.ldb = ldx; g.b_t = true;
-    g.C = i ? dW2 : dW; g.ldc = d;
-    if (gemm(K_FFN_GRADS, g, stream) != cudaSuccess) return LCE_ERR_CUDA;
+// What the launches of one call share.
+struct Call {
+  lce_dtype_t dt;
+  char* ws;
+  int num_sms;
+  cudaStream_t stream;
+
+  cudaError_t few(int kid, const FfnGemm& g) const {
+    return traced(kid, stream, [&] { return launch_ffn_simt(g, stream); });
   }
-  if (dX) {
+  cudaError_t tc(int kid, const FfnTc* jobs, int n) const {
+    return traced(kid, stream, [&] {
+      return launch_ffn_tc(jobs, n, dt, reinterpret_cast<unsigned*>(ws), num_sms, stream);
+    });
+  }
+  // x [rows x cols] as an operand of the tensor-core kernel: itself, or its parts in slot s
+  cudaError_t operand(const void* x, int64_t ld, int64_t rows, int64_t cols, const Slot& s,
+                      FfnOperand* o) const {
+    if (dt == LCE_BF16) {
+      *o = FfnOperand{x, rows, cols, ld, 1, 0};
+      return cudaSuccess;
+    }
+    *o = parts(s, rows, cols);
+    return traced(K_SPLIT_BF16, stream, [&] {
+      return launch_split_bf16(static_cast<const float*>(x), ld, rows, cols, ws + s.off, s.ld,
+                               s.part_stride, stream);
+    });
+  }
+  // an array of the workspace as an operand
+  FfnOperand parts(const Slot& s, int64_t rows, int64_t cols) const {
+    return FfnOperand{ws + s.off, rows, cols, s.ld, dt == LCE_BF16 ? 1 : 3, s.part_stride};
+  }
+};
+
+// dX = dZ W (+ dZ2 W2), dW = dZ^T X (and dW2 = dZ2^T X) in one launch, the longer sums first.
+// nw = 1 or 2 weights; dX or the dW may be null.
+cudaError_t products(const Call& c, const FfnOperand& X, const FfnOperand* W, const FfnOperand* Z,
+                     int nw, int64_t N, int64_t d, int64_t width, void* dX, void* const* dW) {
+  FfnTc jobs[3];
+  int n = 0;
+  auto add_dx = [&] {
+    if (!dX) return;
+    FfnTc& g = jobs[n++] = FfnTc{};
     g.M = N; g.Ncols = d; g.K = width;
-    g.A = dZ; g.lda = ldz; g.a_t = false;
-    g.B = W; g.ldb = d; g.b_t = true;
-    g.A2 = dZ2; g.B2 = W2;
+    g.A = Z[0]; g.B = W[0]; g.b_mn = true;
+    if (nw == 2) { g.A2 = Z[1]; g.B2 = W[1]; }
     g.C = dX; g.ldc = d;
-    if (gemm(K_FFN_GRADS, g, stream) != cudaSuccess) return LCE_ERR_CUDA;
-  }
-  return LCE_OK;
+  };
+  auto add_dw = [&] {
+    for (int i = 0; i < nw && dW[0]; ++i) {
+      FfnTc& g = jobs[n++] = FfnTc{};
+      g.M = width; g.Ncols = d; g.K = N;
+      g.A = Z[i]; g.B = X; g.a_mn = g.b_mn = true;
+      g.C = dW[i]; g.ldc = d;
+    }
+  };
+  if (nw * width >= N) { add_dx(); add_dw(); }
+  else { add_dw(); add_dx(); }
+  if (n == 0) return cudaSuccess;
+  for (int i = 0; i < n; ++i) { jobs[i].mode = FFN_GRADS; jobs[i].act = LCE_ACT_NONE; }
+  return c.tc(K_FFN_GRADS, jobs, n);
 }
 
 }  // namespace
@@ -91,7 +154,7 @@ size_t lce_linear_workspace_size(int64_t N, int64_t d_in, int64_t d_out, lce_act
                                  int32_t backward, lce_dtype_t dtype) {
   if (!dtype_ok(dtype) || !act_ok(activation) || (backward != 0 && backward != 1)) return 0;
   if (!rows_ok(N) || !width_ok(d_in, dtype) || !width_ok(d_out, dtype)) return 0;
-  return layout(N, d_out, (backward && activation != LCE_ACT_NONE) ? 1 : 0, dtype).total;
+  return linear_layout(N, d_in, d_out, activation, backward != 0, dtype).total;
 }
 
 lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const void* bias,
@@ -115,14 +178,30 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
-  FfnGemm g{};
+  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  if (N == 0) return LCE_OK;
+  if (N <= kFewTokens) {
+    FfnGemm g{};
+    g.mode = FFN_LINEAR;
+    g.dtype = dtype; g.act = activation;
+    g.M = N; g.Ncols = d_out; g.K = d_in;
+    g.A = X; g.lda = ldx; g.B = W; g.ldb = d_in;
+    g.bias = bias; g.R = residual; g.ldr = ldr;
+    g.C = Y; g.ldc = ldy;
+    return c.few(K_LIN, g) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  }
+  const Layout L = linear_layout(N, d_in, d_out, activation, false, dtype);
+  FfnTc g{};
   g.mode = FFN_LINEAR;
-  g.dtype = dtype; g.act = activation;
+  g.act = activation;
   g.M = N; g.Ncols = d_out; g.K = d_in;
-  g.A = X; g.lda = ldx; g.B = W; g.ldb = d_in;
   g.bias = bias; g.R = residual; g.ldr = ldr;
   g.C = Y; g.ldc = ldy;
-  return gemm(K_LIN, g, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  if (c.operand(X, ldx, N, d_in, L.x, &g.A) != cudaSuccess ||
+      c.operand(W, d_in, d_out, d_in, L.w[0], &g.B) != cudaSuccess ||
+      c.tc(K_LIN, &g, 1) != cudaSuccess)
+    return LCE_ERR_CUDA;
+  return LCE_OK;
 }
 
 lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, const void* bias,
@@ -151,35 +230,38 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
       return LCE_ERR_CUDA;
     return LCE_OK;
   }
-  const void* dZ = dY;
-  int64_t ldz = ldy;
-  if (activation != LCE_ACT_NONE) {
-    const Layout L = layout(N, d_out, 1, dtype);
-    void* z = static_cast<char*>(workspace) + L.off_z[0];
-    FfnGemm g{};
+  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  const Layout L = linear_layout(N, d_in, d_out, activation, true, dtype);
+  FfnOperand x, w, z;
+  if (c.operand(X, ldx, N, d_in, L.x, &x) != cudaSuccess ||
+      c.operand(W, d_in, d_out, d_in, L.w[0], &w) != cudaSuccess)
+    return LCE_ERR_CUDA;
+  if (activation == LCE_ACT_NONE) {
+    if (c.operand(dY, ldy, N, d_out, L.z[0], &z) != cudaSuccess) return LCE_ERR_CUDA;
+  } else {
+    FfnTc g{};
     g.mode = FFN_LINEAR_DZ;
-    g.dtype = dtype; g.act = activation;
+    g.act = activation;
     g.M = N; g.Ncols = d_out; g.K = d_in;
-    g.A = X; g.lda = ldx; g.B = W; g.ldb = d_in;
+    g.A = x; g.B = w;
     g.bias = bias; g.D = dY; g.ldd = ldy;
-    g.C = z; g.ldc = d_out;
-    if (gemm(K_LIN_DZ, g, stream) != cudaSuccess) return LCE_ERR_CUDA;
-    dZ = z;
-    ldz = d_out;
+    g.C = c.ws + L.z[0].off; g.ldc = L.z[0].ld; g.part_stride = L.z[0].part_stride;
+    if (c.tc(K_LIN_DZ, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
+    z = c.parts(L.z[0], N, d_out);
   }
   if (dbias && traced(K_COLSUM, stream, [&] {
-        return launch_column_sum(dZ, ldz, N, d_out, dtype, dbias, stream);
+        return launch_column_sum(z.ptr, z.ld, N, d_out, dtype, static_cast<int>(z.parts),
+                                 z.part_stride, dbias, stream);
       }) != cudaSuccess)
     return LCE_ERR_CUDA;
-  return products(X, ldx, W, nullptr, dZ, nullptr, ldz, N, d_in, d_out, dtype, dX, dW, nullptr,
-                  stream);
+  return products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
 }
 
 size_t lce_gated_workspace_size(int64_t N, int64_t d, int64_t F, int32_t backward,
                                 lce_dtype_t dtype) {
   if (!dtype_ok(dtype) || (backward != 0 && backward != 1)) return 0;
   if (!rows_ok(N) || !width_ok(d, dtype) || !width_ok(F, dtype)) return 0;
-  return layout(N, F, backward ? 2 : 0, dtype).total;
+  return gated_layout(N, d, F, backward != 0, dtype).total;
 }
 
 lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t N,
@@ -200,13 +282,28 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
-  FfnGemm g{};
+  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  if (N == 0) return LCE_OK;
+  if (N <= kFewTokens) {
+    FfnGemm g{};
+    g.mode = FFN_GATED;
+    g.dtype = dtype; g.act = activation;
+    g.M = N; g.Ncols = F; g.K = d;
+    g.A = X; g.lda = ldx; g.B = Wg; g.B2 = Wu; g.ldb = d;
+    g.C = H; g.ldc = ldh;
+    return c.few(K_GATED, g) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  }
+  const Layout L = gated_layout(N, d, F, false, dtype);
+  FfnTc g{};
   g.mode = FFN_GATED;
-  g.dtype = dtype; g.act = activation;
+  g.act = activation;
   g.M = N; g.Ncols = F; g.K = d;
-  g.A = X; g.lda = ldx; g.B = Wg; g.B2 = Wu; g.ldb = d;
   g.C = H; g.ldc = ldh;
-  return gemm(K_GATED, g, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  if (c.operand(X, ldx, N, d, L.x, &g.A) != cudaSuccess ||
+      c.operand(Wg, d, F, d, L.w[0], &g.B) != cudaSuccess ||
+      c.operand(Wu, d, F, d, L.w[1], &g.B2) != cudaSuccess || c.tc(K_GATED, &g, 1) != cudaSuccess)
+    return LCE_ERR_CUDA;
+  return LCE_OK;
 }
 
 lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, const void* Wu,
@@ -234,17 +331,25 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
       return LCE_ERR_CUDA;
     return LCE_OK;
   }
-  const Layout L = layout(N, F, 2, dtype);
-  char* ws = static_cast<char*>(workspace);
-  FfnGemm g{};
+  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  const Layout L = gated_layout(N, d, F, true, dtype);
+  FfnOperand x, w[2], z[2];
+  if (c.operand(X, ldx, N, d, L.x, &x) != cudaSuccess ||
+      c.operand(Wg, d, F, d, L.w[0], &w[0]) != cudaSuccess ||
+      c.operand(Wu, d, F, d, L.w[1], &w[1]) != cudaSuccess)
+    return LCE_ERR_CUDA;
+  FfnTc g{};
   g.mode = FFN_GATED_DGU;
-  g.dtype = dtype; g.act = activation;
+  g.act = activation;
   g.M = N; g.Ncols = F; g.K = d;
-  g.A = X; g.lda = ldx; g.B = Wg; g.B2 = Wu; g.ldb = d;
+  g.A = x; g.B = w[0]; g.B2 = w[1];
   g.D = dH; g.ldd = ldh;
-  g.C = ws + L.off_z[0]; g.C2 = ws + L.off_z[1]; g.ldc = F;
-  if (gemm(K_GATED_DGU, g, stream) != cudaSuccess) return LCE_ERR_CUDA;
-  return products(X, ldx, Wg, Wu, g.C, g.C2, F, N, d, F, dtype, dX, dWg, dWu, stream);
+  g.C = c.ws + L.z[0].off; g.C2 = c.ws + L.z[1].off;
+  g.ldc = L.z[0].ld; g.part_stride = L.z[0].part_stride;
+  if (c.tc(K_GATED_DGU, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
+  for (int i = 0; i < 2; ++i) z[i] = c.parts(L.z[i], N, F);
+  void* const dW[2] = {dWg, dWu};
+  return products(c, x, w, z, 2, N, d, F, dX, dW) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
 }
 
 }  // extern "C"

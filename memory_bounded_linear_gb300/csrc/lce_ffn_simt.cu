@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "bf16_parts.cuh"
 #include "lce_act.cuh"
 #include "lce_ffn.h"
 #include "lce_internal.h"
@@ -97,13 +98,42 @@ __global__ void __launch_bounds__(256) ffn_simt_kernel(const FfnGemm g) {
 }
 
 // One thread per column, rows in order.
-template <typename E>
-__global__ void column_sum_kernel(const E* x, int64_t ld, int64_t N, int64_t cols, E* out) {
+template <typename E, int PARTS, typename O>
+__global__ void column_sum_kernel(const E* x, int64_t ld, int64_t part_stride, int64_t N, int64_t cols,
+                                  O* out) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (c >= cols) return;
   float s = 0.f;
-  for (int64_t r = 0; r < N; ++r) s += static_cast<float>(x[r * ld + c]);
-  out[c] = static_cast<E>(s);
+  for (int64_t r = 0; r < N; ++r) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = PARTS - 1; k >= 0; --k) v += static_cast<float>(x[k * part_stride + r * ld + c]);
+    s += v;
+  }
+  out[c] = static_cast<O>(s);
+}
+
+// fp32 rows into bf16 parts, four columns per thread.
+__global__ void split_bf16_kernel(const float* x, int64_t ld, int64_t rows, int64_t cols,
+                                  __nv_bfloat16* out, int64_t ld_out, int64_t part_stride) {
+  const int64_t c4 = cols / 4;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * c4;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / c4, c = (i - r * c4) * 4;
+    const float4 v = *reinterpret_cast<const float4*>(x + r * ld + c);
+    float p[4][3];
+    split_bf16(v.x, p[0]);
+    split_bf16(v.y, p[1]);
+    split_bf16(v.z, p[2]);
+    split_bf16(v.w, p[3]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(p[0][k], p[1][k]),
+                             __floats2bfloat162_rn(p[2][k], p[3][k])};
+      *reinterpret_cast<uint2*>(out + k * part_stride + r * ld_out + c) =
+          *reinterpret_cast<uint2*>(h);
+    }
+  }
 }
 
 template <typename E>
@@ -126,14 +156,27 @@ cudaError_t launch_ffn_simt(const FfnGemm& g, cudaStream_t stream) {
 }
 
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, lce_dtype_t dtype,
-                              void* out, cudaStream_t stream) {
+                              int parts, int64_t part_stride, void* out, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((cols + 127) / 128);
-  if (dtype == LCE_BF16)
-    column_sum_kernel<<<blocks, 128, 0, stream>>>(static_cast<const __nv_bfloat16*>(x), ld, N, cols,
-                                                  static_cast<__nv_bfloat16*>(out));
+  const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
+  if (parts == 3)
+    column_sum_kernel<__nv_bfloat16, 3><<<blocks, 128, 0, stream>>>(h, ld, part_stride, N, cols,
+                                                                    static_cast<float*>(out));
+  else if (dtype == LCE_BF16)
+    column_sum_kernel<__nv_bfloat16, 1>
+        <<<blocks, 128, 0, stream>>>(h, ld, 0, N, cols, static_cast<__nv_bfloat16*>(out));
   else
-    column_sum_kernel<<<blocks, 128, 0, stream>>>(static_cast<const float*>(x), ld, N, cols,
-                                                  static_cast<float*>(out));
+    column_sum_kernel<float, 1><<<blocks, 128, 0, stream>>>(static_cast<const float*>(x), ld, 0, N, cols,
+                                                            static_cast<float*>(out));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_split_bf16(const float* x, int64_t ld, int64_t rows, int64_t cols, void* out,
+                              int64_t ld_out, int64_t part_stride, cudaStream_t stream) {
+  const int64_t need = (rows * (cols / 4) + 255) / 256;
+  const unsigned blocks = static_cast<unsigned>(need < 152 * 16 ? need : 152 * 16);
+  split_bf16_kernel<<<blocks, 256, 0, stream>>>(x, ld, rows, cols, static_cast<__nv_bfloat16*>(out),
+                                                ld_out, part_stride);
   return cudaGetLastError();
 }
 

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblce.so")
 
 SOURCES = ["lce_api.cu", "lce_tc.cu", "lce_simt.cu", "lce_reduce.cu", "lce_static_scratch.cu",
-           "lce_ffn_api.cu", "lce_ffn_simt.cu", "lce_ffn_tc.cu",
+           "lce_ffn_api.cu", "lce_ffn_few.cu", "lce_ffn_simt.cu", "lce_ffn_tc.cu",
            "lce_gradnorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -18,21 +18,17 @@ enum FfnMode : int {
   FFN_GRADS = 4,      // C = Z, or Z + A2 B2^T (two pairs of operands into one sum)
 };
 
-// One product.  Strides in elements; an operand is row-major [rows x K], or with *_t set stored
-// as [K x rows] (the contracted index is its row).
+// A forward product of a few tokens (FFN_LINEAR or FFN_GATED): A is X [M x K], B (and B2) the weights
+// [Ncols x K], all row-major with strides in elements.
 struct FfnGemm {
   int mode;
-  lce_dtype_t dtype;
   lce_activation_t act;
   int64_t M, Ncols, K;
-  const void* A; int64_t lda; bool a_t;
-  const void* B; int64_t ldb; bool b_t;
-  const void* A2; const void* B2;  // gated: B2 only; FFN_GRADS: the second pair, or null
+  const void* A; int64_t lda;
+  const void* B; const void* B2; int64_t ldb;
   const void* bias;                // [Ncols] or null
-  const void* R; int64_t ldr;      // FFN_LINEAR: residual, or null
-  const void* D; int64_t ldd;      // outgoing gradient [M x Ncols]
+  const void* R; int64_t ldr;      // residual, or null
   void* C; int64_t ldc;
-  void* C2;                        // FFN_GATED_DGU (row stride ldc)
 };
 
 // An operand of the tensor-core kernel as it is stored: bf16 rows of stored_cols elements, ld
@@ -43,7 +39,8 @@ struct FfnOperand {
   int64_t parts, part_stride;
 };
 
-// One product for the tensor-core kernel; fields as in FfnGemm.  a_mn / b_mn: stored [K x rows].
+// One product for the tensor-core kernel.  a_mn / b_mn: stored [K x rows]; A2, B2: the second weights
+// (gated), or a second pair of operands summed into the same product (FFN_GRADS; ptr null: none).
 // For LCE_F32 the pre-activation gradients C and C2 are written as bf16 parts (row stride ldc,
 // part_stride apart), and C of the other modes as fp32.
 struct FfnTc {
@@ -66,11 +63,14 @@ cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsig
 // fp32 x [rows x cols], row stride ld, into three bf16 parts of row stride ld_out: lce_ffn_simt.cu
 cudaError_t launch_split_bf16(const float* x, int64_t ld, int64_t rows, int64_t cols, void* out,
                               int64_t ld_out, int64_t part_stride, cudaStream_t stream);
-// CUDA cores, any mode, type and layout: lce_ffn_simt.cu
-cudaError_t launch_ffn_simt(const FfnGemm& g, cudaStream_t stream);
-// out[c] = sum over the N rows of x[., c], row stride ld; parts = 3: x holds three bf16 parts,
-// part_stride apart, and out is fp32: lce_ffn_simt.cu
-cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, lce_dtype_t dtype,
-                              int parts, int64_t part_stride, void* out, cudaStream_t stream);
+// Few tokens, bf16 (at most FFN_FEW_TOKENS rows): lce_ffn_few.cu.  Clears the error flags.
+constexpr int64_t FFN_FEW_TOKENS = 128;
+cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream);
+// Few tokens, fp32: lce_ffn_simt.cu.  Clears the error flags.
+cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream);
+// out[c] = sum over the N rows of x[., c], row stride ld.  parts = 1: x and out bf16; parts = 3: x
+// holds three bf16 parts, part_stride apart, and out is fp32: lce_ffn_simt.cu
+cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
+                              int64_t part_stride, void* out, cudaStream_t stream);
 
 }  // namespace lce

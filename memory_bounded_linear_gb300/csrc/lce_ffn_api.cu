@@ -27,9 +27,9 @@ bool width_ok(int64_t w, lce_dtype_t dt) {
 }
 bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
 
-// Products of at most this many tokens (forward) run on the CUDA-core kernel, larger ones on the
-// tensor cores, whose tiles hold 256 tokens.
-constexpr int64_t kFewTokens = 128;
+// Forward products of at most so many tokens run as a weight stream (lce_ffn_few.cu, and for fp32
+// lce_ffn_simt.cu), larger ones on the kernel whose tiles hold 256 tokens.
+bool few_tokens(int64_t N, lce_dtype_t dt) { return N <= (dt == LCE_BF16 ? FFN_FEW_TOKENS : 32); }
 
 int64_t round8(int64_t x) { return (x + 7) & ~int64_t(7); }
 
@@ -57,7 +57,7 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
     s.part_stride = rows * s.ld;
     off += align256(static_cast<size_t>(s.part_stride) * 2 * (dt == LCE_BF16 ? 1 : 3));
   };
-  if (dt == LCE_F32 && (backward || N > kFewTokens)) {
+  if (dt == LCE_F32 && (backward || !few_tokens(N, dt))) {
     take(L.x, N, d);
     for (int i = 0; i < weights; ++i) take(L.w[i], width, d);
   }
@@ -88,7 +88,11 @@ struct Call {
   cudaStream_t stream;
 
   cudaError_t few(int kid, const FfnGemm& g) const {
-    return traced(kid, stream, [&] { return launch_ffn_simt(g, stream); });
+    return traced(kid, stream, [&] {
+      unsigned* err = reinterpret_cast<unsigned*>(ws);
+      return dt == LCE_BF16 ? launch_ffn_few(g, err, num_sms, stream)
+                            : launch_ffn_few_f32(g, err, stream);
+    });
   }
   cudaError_t tc(int kid, const FfnTc* jobs, int n) const {
     return traced(kid, stream, [&] {
@@ -177,13 +181,15 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
+  // the kernels for a few tokens clear the error flags themselves
+  if ((N == 0 || !few_tokens(N, dtype)) && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess)
+    return LCE_ERR_CUDA;
   const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   if (N == 0) return LCE_OK;
-  if (N <= kFewTokens) {
+  if (few_tokens(N, dtype)) {
     FfnGemm g{};
     g.mode = FFN_LINEAR;
-    g.dtype = dtype; g.act = activation;
+    g.act = activation;
     g.M = N; g.Ncols = d_out; g.K = d_in;
     g.A = X; g.lda = ldx; g.B = W; g.ldb = d_in;
     g.bias = bias; g.R = residual; g.ldr = ldr;
@@ -250,8 +256,8 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
     z = c.parts(L.z[0], N, d_out);
   }
   if (dbias && traced(K_COLSUM, stream, [&] {
-        return launch_column_sum(z.ptr, z.ld, N, d_out, dtype, static_cast<int>(z.parts),
-                                 z.part_stride, dbias, stream);
+        return launch_column_sum(z.ptr, z.ld, N, d_out, static_cast<int>(z.parts), z.part_stride,
+                                 dbias, stream);
       }) != cudaSuccess)
     return LCE_ERR_CUDA;
   return products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
@@ -281,13 +287,15 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
+  // the kernels for a few tokens clear the error flags themselves
+  if ((N == 0 || !few_tokens(N, dtype)) && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess)
+    return LCE_ERR_CUDA;
   const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   if (N == 0) return LCE_OK;
-  if (N <= kFewTokens) {
+  if (few_tokens(N, dtype)) {
     FfnGemm g{};
     g.mode = FFN_GATED;
-    g.dtype = dtype; g.act = activation;
+    g.act = activation;
     g.M = N; g.Ncols = F; g.K = d;
     g.A = X; g.lda = ldx; g.B = Wg; g.B2 = Wu; g.ldb = d;
     g.C = H; g.ldc = ldh;

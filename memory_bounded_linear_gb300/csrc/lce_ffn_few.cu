@@ -1,0 +1,342 @@
+// Feed-forward products of a few tokens (decoding), bf16: Y = act(X W^T + b) + R and
+// H = act(X Wg^T) * (X Wu^T) for at most FFN_FEW_TOKENS rows of X.
+//
+// The weights are read once and little else, so the kernel is a weight stream: bound by HBM.  The
+// tensor cores take the weights as their 128-row operand and the tokens as the columns
+// (D[128 features x NT tokens] = W_tile X^T, NT = 16, 32, 64 or 128, tokens past N zero-filled by
+// TMA), so one kernel serves one token and a hundred at the same bytes.
+//   warp 0      TMA producer: k-blocks of 64 of the weight rows (of Wg and Wu both) and of X through
+//               a ring of about 100 KB, two CTAs per SM: 200 KB in flight per SM
+//   warp 1      MMA issuer (tcgen05, cta_group::1, M = 128, N = NT), accumulators in TMEM
+//   warps 2..5  epilogue: thread = feature, so a token's results leave as 64 contiguous bytes a warp
+// With few row tiles the K loop is split over a cluster of S = 2, 4 or 8 CTAs; each puts its fp32
+// partial sums into its shared memory and adds up every S-th token from all of them, in rank order,
+// through distributed shared memory: no second launch, no atomics, a fixed order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "lce_act.cuh"
+#include "lce_ffn.h"
+#include "lce_internal.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace lce {
+namespace {
+
+constexpr int BK = 64;
+constexpr int THREADS = 192;
+constexpr int RING_BYTES = 110 * 1024;     // two CTAs per SM
+constexpr int WIDE_RING_BYTES = 200 * 1024;  // where the partial sums leave room for one only
+constexpr int MAX_STAGES = 8;
+constexpr int CTL_BYTES = 256;
+constexpr int MAX_SPLIT = 8;
+
+template <int NT, bool GATED>
+struct Cfg {
+  static constexpr int W_BYTES = BM * 128;
+  static constexpr int X_BYTES = NT * 128;
+  static constexpr int STAGE_BYTES = (GATED ? 2 : 1) * W_BYTES + X_BYTES;
+  static constexpr int PART_BYTES = (GATED ? 2 : 1) * NT * BM * 4;  // one CTA's partial sums
+  static constexpr int BUDGET = PART_BYTES <= RING_BYTES ? RING_BYTES : WIDE_RING_BYTES;
+  static constexpr int STAGES = BUDGET / STAGE_BYTES < MAX_STAGES ? BUDGET / STAGE_BYTES : MAX_STAGES;
+  static constexpr int RING = STAGES * STAGE_BYTES > PART_BYTES ? STAGES * STAGE_BYTES : PART_BYTES;
+  static constexpr int SMEM_BYTES = RING + 1024 + CTL_BYTES;
+  static constexpr int COLS = (GATED ? 2 : 1) * NT;
+  static constexpr int TMEM = COLS < 32 ? 32 : COLS;  // a power of two
+};
+
+struct Ctl {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block too large");
+
+struct Maps {
+  CUtensorMap w, w2, x;
+};
+
+struct Params {
+  int N, width, nkb, split;
+  int act;
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* R; int64_t ldr;
+  __nv_bfloat16* Y; int64_t ldy;
+  unsigned* err;
+};
+
+// One result: feature f of token t.
+template <int ACT, bool GATED>
+__device__ __forceinline__ void finish(const Params& p, int t, int f, float z, float u, float b) {
+  float v;
+  if (GATED) {
+    v = act<ACT, true>(z) * u;
+  } else {
+    v = act<ACT, true>(z + b);
+    if (p.R) v += __bfloat162float(p.R[t * p.ldr + f]);
+  }
+  p.Y[t * p.ldy + f] = __float2bfloat16_rn(v);
+}
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant__ Maps maps,
+                                                          const Params p) {
+  using Cf = Cfg<NT, GATED>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw_addr);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + Cf::RING);
+  volatile int* abort_flag = &ctl->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    // The workspace's error flags: the first CTA is among the first to run, and a wait gives up only
+    // WAIT_LIMIT_NS after that.
+    if (blockIdx.x == 0) *p.err = 0u;
+    for (int s = 0; s < Cf::STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
+    }
+    ptx::mbar_init(ptx::smem_addr(&ctl->done), 1);
+    ctl->abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), Cf::TMEM);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring r{0, 0u};
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t full = ptx::smem_addr(&ctl->full[r.stage]);
+        if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(full, Cf::STAGE_BYTES);
+        const uint32_t s0 = base + r.stage * Cf::STAGE_BYTES;
+        ptx::tma_load_2d(s0, &maps.w, kb * BK, tile * BM, full);
+        if (GATED) ptx::tma_load_2d(s0 + Cf::W_BYTES, &maps.w2, kb * BK, tile * BM, full);
+        ptx::tma_load_2d(s0 + Cf::STAGE_BYTES - Cf::X_BYTES, &maps.x, kb * BK, 0, full);
+        if (++r.stage == Cf::STAGES) { r.stage = 0; r.ph ^= 1u; }
+      }
+      if (!ok) {  // let copies already in flight land before the CTA can exit
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 2000000ull) {}
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_bf16_f32(BM, NT, false, false);
+      Ring r{0, 0u};
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bar(ptx::smem_addr(&ctl->full[r.stage]), r.ph, abort_flag, p.err)) break;
+        ptx::tc_fence_after();
+        const uint32_t s0 = base + r.stage * Cf::STAGE_BYTES;
+        const uint32_t sx = s0 + Cf::STAGE_BYTES - Cf::X_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) {
+          const uint32_t acc = (kb != kb0 || k != 0) ? 1u : 0u;
+          ptx::tc_mma_f16(tmem_base, desc_kmajor(s0, k), desc_kmajor(sx, k), IDESC, acc);
+          if (GATED)
+            ptx::tc_mma_f16(tmem_base + NT, desc_kmajor(s0 + Cf::W_BYTES, k), desc_kmajor(sx, k),
+                            IDESC, acc);
+        }
+        ptx::tc_commit(ptx::smem_addr(&ctl->empty[r.stage]));
+        if (++r.stage == Cf::STAGES) { r.stage = 0; r.ph ^= 1u; }
+      }
+      // the accumulators are complete (after a timeout: no MMA is still writing them)
+      ptx::tc_commit(ptx::smem_addr(&ctl->done));
+    }
+    __syncwarp();
+  }
+
+  const int q = warp & 3;
+  const int feature = q * 32 + lane;
+  const int f = tile * BM + feature;
+  const bool epilogue = warp >= 2;
+  const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+  float b = 0.f;
+  if (epilogue) {
+    if (!GATED && p.bias && f < p.width) b = __bfloat162float(p.bias[f]);
+    // bounded like every wait; after an abort the results are worthless, the flag says so
+    wait_bar_drain(ptx::smem_addr(&ctl->done), 0, WAIT_LIMIT_NS + WAIT_LIMIT_NS / 2);
+    ptx::tc_fence_after();
+    if (p.split == 1) {
+      dispatch_act(p.act, [&](auto tag) {
+#pragma unroll 1
+        for (int c = 0; c < NT && c < p.N; c += 16) {
+          float z[16], u[16];
+          ptx::tmem_load16(tbase + c, z);
+          if (GATED) ptx::tmem_load16(tbase + NT + c, u);
+          if (f < p.width) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < p.N)
+                finish<decltype(tag)::value, GATED>(p, c + j, f, z[j], GATED ? u[j] : 0.f, b);
+          }
+        }
+      });
+    } else {
+      // every load of the ring has been read by an MMA: its memory holds the partial sums now
+      float* part = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+      for (int c = 0; c < NT && c < p.N; c += 16) {
+        float z[16];
+#pragma unroll
+        for (int g = 0; g < (GATED ? 2 : 1); ++g) {
+          ptx::tmem_load16(tbase + g * NT + c, z);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[(g * NT + c + j) * BM + feature] = z[j];
+        }
+      }
+    }
+  }
+  if (p.split > 1) {
+    __syncwarp();
+    ptx::cluster_sync();
+    if (epilogue && f < p.width) {
+      uint32_t peer[MAX_SPLIT];
+#pragma unroll
+      for (int s = 0; s < MAX_SPLIT; ++s)
+        peer[s] = ptx::mapa_shared(base + feature * 4, s < p.split ? s : 0);
+      dispatch_act(p.act, [&](auto tag) {
+#pragma unroll 1
+        for (int t = rank; t < p.N; t += p.split) {
+          float v[GATED ? 2 : 1][MAX_SPLIT];
+#pragma unroll
+          for (int g = 0; g < (GATED ? 2 : 1); ++g)
+#pragma unroll
+            for (int s = 0; s < MAX_SPLIT; ++s)
+              v[g][s] = s < p.split ? ptx::ld_shared_cluster(peer[s] + (g * NT + t) * BM * 4) : 0.f;
+          float z = 0.f, u = 0.f;
+#pragma unroll
+          for (int s = 0; s < MAX_SPLIT; ++s) {
+            z += v[0][s];
+            if (GATED) u += v[GATED ? 1 : 0][s];
+          }
+          finish<decltype(tag)::value, GATED>(p, t, f, z, u, b);
+        }
+      });
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // no CTA leaves while another reads its partial sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, Cf::TMEM);
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) {
+    set_error_detail("cuTensorMapEncodeTiled entry point unavailable");
+    return false;
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides,
+                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error_detail("tensor map of a few-token operand refused (CUresult %d; %lld x %lld elements,"
+                     " row stride %lld, address %p)",
+                     static_cast<int>(r), static_cast<long long>(outer),
+                     static_cast<long long>(inner), static_cast<long long>(ld), ptr);
+    return false;
+  }
+  return true;
+}
+
+template <int NT, bool GATED>
+cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
+  using Cf = Cfg<NT, GATED>;
+  static bool attr_set = false;
+  if (!attr_set) {
+    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<NT, GATED>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
+    if (e != cudaSuccess) {
+      set_error_detail("shared-memory attribute of the few-token kernel: %s", cudaGetErrorName(e));
+      return e;
+    }
+    attr_set = true;
+  }
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!make_map(&maps.w, g.B, g.K, g.Ncols, g.ldb, BM) ||
+      !make_map(&maps.x, g.A, g.K, g.M, g.lda, NT) ||
+      (GATED && !make_map(&maps.w2, g.B2, g.K, g.Ncols, g.ldb, BM)))
+    return cudaErrorInvalidResourceHandle;
+  Params p{};
+  p.N = static_cast<int>(g.M);
+  p.width = static_cast<int>(g.Ncols);
+  p.nkb = static_cast<int>((g.K + BK - 1) / BK);
+  p.act = g.act;
+  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+  p.R = static_cast<const __nv_bfloat16*>(g.R); p.ldr = g.ldr;
+  p.Y = static_cast<__nv_bfloat16*>(g.C); p.ldy = g.ldc;
+  p.err = err;
+  // Split K until two CTAs per SM are filled, keeping at least four k-blocks for each.
+  const int64_t tiles = (g.Ncols + BM - 1) / BM;
+  p.split = 1;
+  while (p.split < MAX_SPLIT && tiles * p.split * 2 <= 2 * num_sms && p.nkb >= 8 * p.split) p.split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<NT, GATED>, maps, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess)
+    set_error_detail("launch of the few-token kernel (%lld tiles, split %d): %s",
+                     static_cast<long long>(tiles), p.split, cudaGetErrorName(e));
+  return e;
+}
+
+template <bool GATED>
+cudaError_t pick(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
+  if (g.M <= 16) return launch<16, GATED>(g, err, num_sms, stream);
+  if (g.M <= 32) return launch<32, GATED>(g, err, num_sms, stream);
+  if (g.M <= 64) return launch<64, GATED>(g, err, num_sms, stream);
+  return launch<128, GATED>(g, err, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
+  return g.mode == FFN_GATED ? pick<true>(g, err, num_sms, stream)
+                             : pick<false>(g, err, num_sms, stream);
+}
+
+}  // namespace lce

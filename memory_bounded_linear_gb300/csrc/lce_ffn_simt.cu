@@ -1,6 +1,5 @@
-// Feed-forward products on the CUDA cores: one kernel for every mode, type and operand layout.
-// A block computes a 64 x 64 tile of Z (and of Z2) with 4 x 4 outputs per thread, k-blocks of 16
-// through shared memory, fp32 FMA; the epilogue is elementwise on the accumulators.
+// CUDA-core kernels of the feed-forward operators: fp32 products of a few tokens, column sums
+// (dbias), and the split of fp32 operands into bf16 parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -13,90 +12,94 @@
 namespace lce {
 namespace {
 
-constexpr int T = 64, KB = 16;
+// ---------------------------------------------------------------- fp32 products of a few tokens
+// Bound by reading the weights once (HBM).  A block computes ROWS features (of Wg and Wu both, when
+// gated) for NT tokens; its eight warps take 512-byte pieces of K in turn, lanes four elements each,
+// and each weight vector loaded serves NT tokens from registers (X comes from L1/L2).  The lanes'
+// sums meet by shuffles, the warps' in shared memory, in a fixed order.
+constexpr int WARPS = 8;
+constexpr int ROWS = 4;
 
-template <typename E>
-__device__ __forceinline__ float ld(const void* p, int64_t i) {
-  return static_cast<float>(static_cast<const E*>(p)[i]);
-}
-
-template <typename E, int MODE>
-__global__ void __launch_bounds__(256) ffn_simt_kernel(const FfnGemm g) {
-  constexpr bool DUAL = MODE == FFN_GATED || MODE == FFN_GATED_DGU;
-  constexpr bool FAST = sizeof(E) == 2;
-  __shared__ float sa[KB][T + 4], sb[KB][T + 4], sb2[DUAL ? KB : 1][T + 4];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * T, n0 = static_cast<int64_t>(blockIdx.y) * T;
-  float z[4][4] = {}, z2[4][4] = {};
-  const int pairs = (MODE == FFN_GRADS && g.A2) ? 2 : 1;
-  for (int pair = 0; pair < pairs; ++pair) {
-    const void* A = pair ? g.A2 : g.A;
-    const void* B = pair ? g.B2 : g.B;
-    for (int64_t k0 = 0; k0 < g.K; k0 += KB) {
-      for (int i = threadIdx.x; i < T * KB; i += 256) {
-        // neighbouring threads walk the operand's contiguous index
-        const int ka = g.a_t ? i / T : i % KB, ra = g.a_t ? i % T : i / KB;
-        const int64_t m = m0 + ra, k = k0 + ka;
-        sa[ka][ra] = (m < g.M && k < g.K) ? ld<E>(A, g.a_t ? k * g.lda + m : m * g.lda + k) : 0.f;
-        const int kb = g.b_t ? i / T : i % KB, rb = g.b_t ? i % T : i / KB;
-        const int64_t n = n0 + rb, kk = k0 + kb;
-        const bool ok = n < g.Ncols && kk < g.K;
-        const int64_t off = g.b_t ? kk * g.ldb + n : n * g.ldb + kk;
-        sb[kb][rb] = ok ? ld<E>(B, off) : 0.f;
-        if (DUAL) sb2[kb][rb] = ok ? ld<E>(g.B2, off) : 0.f;
-      }
-      __syncthreads();
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
+                                                             unsigned* err) {
+  constexpr int R = GATED ? 2 * ROWS : ROWS;
+  __shared__ float sh[WARPS][R * NT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0u;  // this kernel never waits
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * NT;
+  const float* X = static_cast<const float*>(g.A);
+  const float* w[R];
+  const float* x[NT];
 #pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        float a[4], b[4], b2[4];
+  for (int r = 0; r < R; ++r) {
+    // features and tokens past the end repeat the last one; their results are dropped
+    const int64_t f = min(f0 + r % ROWS, g.Ncols - 1);
+    w[r] = static_cast<const float*>(r < ROWS ? g.B : g.B2) + f * g.ldb;
+  }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = sa[k][ty * 4 + i];
-          b[i] = sb[k][tx * 4 + i];
-          if (DUAL) b2[i] = sb2[k][tx * 4 + i];
-        }
+  for (int t = 0; t < NT; ++t) x[t] = X + min(t0 + t, g.M - 1) * g.lda;
+  float acc[R][NT] = {};
+  for (int64_t k = (warp * 32 + lane) * 4; k < g.K; k += WARPS * 128) {
+    float4 wv[R];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int r = 0; r < R; ++r) wv[r] = __ldcs(reinterpret_cast<const float4*>(w[r] + k));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z[i][j] = fmaf(a[i], b[j], z[i][j]);
-            if (DUAL) z2[i][j] = fmaf(a[i], b2[j], z2[i][j]);
-          }
-      }
-      __syncthreads();
+    for (int t = 0; t < NT; ++t) {
+      const float4 xv = __ldg(reinterpret_cast<const float4*>(x[t] + k));
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        acc[r][t] = fmaf(wv[r].x, xv.x, fmaf(wv[r].y, xv.y, fmaf(wv[r].z, xv.z, fmaf(wv[r].w, xv.w, acc[r][t]))));
     }
   }
-  E* C = static_cast<E*>(g.C);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float v = acc[r][t];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) sh[warp][r * NT + t] = v;
+    }
+  __syncthreads();
+  const int i = threadIdx.x;  // one result per thread
+  if (i >= ROWS * NT) return;
+  const int r = i % ROWS, t = i / ROWS;
+  const int64_t f = f0 + r, m = t0 + t;
+  if (f >= g.Ncols || m >= g.M) return;
+  float z = 0.f, u = 0.f;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) {
+    z += sh[k][r * NT + t];
+    if (GATED) u += sh[k][(ROWS + r) * NT + t];
+  }
+  float v;
   dispatch_act(g.act, [&](auto tag) {
     constexpr int ACT = decltype(tag)::value;
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (m >= g.M || n >= g.Ncols) continue;
-        const int64_t c = m * g.ldc + n;
-        float v = z[i][j];
-        if ((MODE == FFN_LINEAR || MODE == FFN_LINEAR_DZ) && g.bias) v += ld<E>(g.bias, n);
-        if (MODE == FFN_LINEAR) {
-          v = act<ACT, FAST>(v);
-          if (g.R) v += ld<E>(g.R, m * g.ldr + n);
-        } else if (MODE == FFN_GATED) {
-          v = act<ACT, FAST>(v) * z2[i][j];
-        } else if (MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU) {
-          float a, d;
-          act_grad<ACT, FAST>(v, a, d);
-          const float o = ld<E>(g.D, m * g.ldd + n);
-          if (DUAL) {
-            static_cast<E*>(g.C2)[c] = static_cast<E>(o * a);
-            v = o * z2[i][j] * d;
-          } else {
-            v = o * d;
-          }
-        }
-        C[c] = static_cast<E>(v);
-      }
+    if (GATED) {
+      v = act<ACT, false>(z) * u;
+    } else {
+      if (g.bias) z += static_cast<const float*>(g.bias)[f];
+      v = act<ACT, false>(z);
+      if (g.R) v += static_cast<const float*>(g.R)[m * g.ldr + f];
+    }
   });
+  static_cast<float*>(g.C)[m * g.ldc + f] = v;
 }
 
+template <bool GATED>
+cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
+  const unsigned bx = static_cast<unsigned>((g.Ncols + ROWS - 1) / ROWS);
+  const auto by = [&](int nt) { return dim3(bx, static_cast<unsigned>((g.M + nt - 1) / nt)); };
+  if (g.M == 1) few_f32_kernel<1, GATED><<<by(1), WARPS * 32, 0, stream>>>(g, err);
+  else if (g.M == 2) few_f32_kernel<2, GATED><<<by(2), WARPS * 32, 0, stream>>>(g, err);
+  else if (g.M <= 4) few_f32_kernel<4, GATED><<<by(4), WARPS * 32, 0, stream>>>(g, err);
+  else few_f32_kernel<8, GATED><<<by(8), WARPS * 32, 0, stream>>>(g, err);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------- column sums
 // One thread per column, rows in order.
 template <typename E, int PARTS, typename O>
 __global__ void column_sum_kernel(const E* x, int64_t ld, int64_t part_stride, int64_t N, int64_t cols,
@@ -136,38 +139,22 @@ __global__ void split_bf16_kernel(const float* x, int64_t ld, int64_t rows, int6
   }
 }
 
-template <typename E>
-cudaError_t simt(const FfnGemm& g, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((g.M + T - 1) / T), static_cast<unsigned>((g.Ncols + T - 1) / T));
-  switch (g.mode) {
-    case FFN_LINEAR: ffn_simt_kernel<E, FFN_LINEAR><<<grid, 256, 0, stream>>>(g); break;
-    case FFN_GATED: ffn_simt_kernel<E, FFN_GATED><<<grid, 256, 0, stream>>>(g); break;
-    case FFN_LINEAR_DZ: ffn_simt_kernel<E, FFN_LINEAR_DZ><<<grid, 256, 0, stream>>>(g); break;
-    case FFN_GATED_DGU: ffn_simt_kernel<E, FFN_GATED_DGU><<<grid, 256, 0, stream>>>(g); break;
-    default: ffn_simt_kernel<E, FFN_GRADS><<<grid, 256, 0, stream>>>(g);
-  }
-  return cudaGetLastError();
-}
-
 }  // namespace
 
-cudaError_t launch_ffn_simt(const FfnGemm& g, cudaStream_t stream) {
-  return g.dtype == LCE_BF16 ? simt<__nv_bfloat16>(g, stream) : simt<float>(g, stream);
+cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
+  return g.mode == FFN_GATED ? few_f32<true>(g, err, stream) : few_f32<false>(g, err, stream);
 }
 
-cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, lce_dtype_t dtype,
-                              int parts, int64_t part_stride, void* out, cudaStream_t stream) {
+cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
+                              int64_t part_stride, void* out, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((cols + 127) / 128);
   const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
   if (parts == 3)
     column_sum_kernel<__nv_bfloat16, 3><<<blocks, 128, 0, stream>>>(h, ld, part_stride, N, cols,
                                                                     static_cast<float*>(out));
-  else if (dtype == LCE_BF16)
+  else
     column_sum_kernel<__nv_bfloat16, 1>
         <<<blocks, 128, 0, stream>>>(h, ld, 0, N, cols, static_cast<__nv_bfloat16*>(out));
-  else
-    column_sum_kernel<float, 1><<<blocks, 128, 0, stream>>>(static_cast<const float*>(x), ld, 0, N, cols,
-                                                            static_cast<float*>(out));
   return cudaGetLastError();
 }
 

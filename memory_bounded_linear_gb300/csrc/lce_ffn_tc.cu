@@ -20,7 +20,11 @@
 // fp32 operands come as three bf16 parts x = p0 + p1 + p2 (8 bits each, together the 24 of x), and
 // a product is the sum of six part products, smallest first: p2 q0, p0 q2, p1 q1, p1 q0, p0 q1,
 // p0 q0; the three that are left out are below 2^-24 of the product.  To the kernel that is a K
-// loop six times as long, the part being the third coordinate of the operand's tensor map.
+// loop six times as long, the part being the third coordinate of the operand's tensor map.  The
+// tensor cores cut each addition into an accumulator off rather than round it, an error that grows
+// with the number of additions (2.6e-6 of a sum of 2008 products); so an fp32 tile is summed in
+// steps of F32_STEP k-blocks, each into a fresh accumulator, which the epilogue warps add up in
+// registers (4e-7 there, for a drain of about 1,000 cycles per 12,000 of products).
 //
 // The outgoing gradient D and the residual R enter, and C leaves, through one 4 KB box per epilogue
 // warp (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
@@ -56,6 +60,7 @@ constexpr int CTL_BYTES = 512;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES + 1024 + CTL_BYTES;
 constexpr int RASTER = 8;               // row tiles per rasterisation group (as in lce_tc.cu)
 constexpr int MAX_JOBS = 3;
+constexpr int F32_STEP = 4;             // k-blocks per accumulator of an fp32 tile
 static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
 
 struct Ctl {
@@ -125,40 +130,53 @@ __device__ __forceinline__ TilePos locate(const KParams& p, int t) {
   return r;
 }
 
-// Producer side of one tile.  MN: both operands MN-major; B_MN: B MN-major.
+// A tile's K loop as steps, one accumulator each: bf16 a single step over all operand pairs, fp32
+// F32_STEP k-blocks of one pair at a time.
+template <bool F32>
+__device__ __forceinline__ int steps_of(int nkb, int pairs) {
+  return F32 ? pairs * ((nkb + F32_STEP - 1) / F32_STEP) : 1;
+}
+
+// Producer side of one tile.  A_MN, B_MN: the operand is MN-major.
 template <bool A_MN, bool B_MN, bool F32>
 __device__ __forceinline__ bool produce_tile(int nkb, int pairs, const CUtensorMap* mA,
                                              const CUtensorMap* mB, int m0, int n0, uint32_t base,
                                              Ctl* ctl, Ring& r, volatile int* abort_flag,
                                              unsigned* err, uint32_t rank) {
-  for (int s = F32 ? 0 : 5; s < 6; ++s) {
-    const int za = part_a(s), zb = part_b(s);
-    for (int pr = 0; pr < pairs; ++pr) {
-      const CUtensorMap* a = &mA[pr];
-      const CUtensorMap* b = &mB[pr];
-      for (int kb = 0; kb < nkb; ++kb) {
-        const uint32_t full_local = ptx::smem_addr(&ctl->full[r.stage]);
-        if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, err)) return false;
-        const uint32_t full = ptx::mapa_shared(full_local, 0);
-        if (rank == 0) ptx::mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
-        const uint32_t sa = base + r.stage * STAGE_BYTES, sb = sa + A_BYTES;
-        const int k0 = kb * BK;
-        if (A_MN) {
+  auto block = [&](const CUtensorMap* a, const CUtensorMap* b, int k0, int za, int zb) {
+    const uint32_t full_local = ptx::smem_addr(&ctl->full[r.stage]);
+    if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, err)) return false;
+    const uint32_t full = ptx::mapa_shared(full_local, 0);
+    if (rank == 0) ptx::mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
+    const uint32_t sa = base + r.stage * STAGE_BYTES, sb = sa + A_BYTES;
+    if (A_MN) {
 #pragma unroll
-          for (int c = 0; c < BM / MN_BOX_ELEMS; ++c)
-            ptx::tma_load_3d_pair(sa + c * MN_BOX_BYTES, a, m0 + c * MN_BOX_ELEMS, k0, za, full);
-        } else {
-          ptx::tma_load_3d_pair(sa, a, k0, m0, za, full);
-        }
-        if (B_MN) {
+      for (int c = 0; c < BM / MN_BOX_ELEMS; ++c)
+        ptx::tma_load_3d_pair(sa + c * MN_BOX_BYTES, a, m0 + c * MN_BOX_ELEMS, k0, za, full);
+    } else {
+      ptx::tma_load_3d_pair(sa, a, k0, m0, za, full);
+    }
+    if (B_MN) {
 #pragma unroll
-          for (int c = 0; c < HALF / MN_BOX_ELEMS; ++c)
-            ptx::tma_load_3d_pair(sb + c * MN_BOX_BYTES, b, n0 + c * MN_BOX_ELEMS, k0, zb, full);
-        } else {
-          ptx::tma_load_3d_pair(sb, b, k0, n0, zb, full);
-        }
-        if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
-      }
+      for (int c = 0; c < HALF / MN_BOX_ELEMS; ++c)
+        ptx::tma_load_3d_pair(sb + c * MN_BOX_BYTES, b, n0 + c * MN_BOX_ELEMS, k0, zb, full);
+    } else {
+      ptx::tma_load_3d_pair(sb, b, k0, n0, zb, full);
+    }
+    if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
+    return true;
+  };
+  for (int pr = 0; pr < pairs; ++pr) {
+    const CUtensorMap* a = &mA[pr];
+    const CUtensorMap* b = &mB[pr];
+    if (!F32) {
+      for (int kb = 0; kb < nkb; ++kb)
+        if (!block(a, b, kb * BK, 0, 0)) return false;
+    } else {
+      for (int kb0 = 0; kb0 < nkb; kb0 += F32_STEP)
+        for (int s = 0; s < 6; ++s)
+          for (int kb = kb0; kb < min(nkb, kb0 + F32_STEP); ++kb)
+            if (!block(a, b, kb * BK, part_a(s), part_b(s))) return false;
     }
   }
   return true;
@@ -188,6 +206,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// The four 32-column groups of accumulator columns that a warp of column half `half` drains.
+template <bool GATED>
+__device__ __forceinline__ int half_col(int half, int h) {
+  return GATED ? (h >> 1) * HALF + half * (HALF / 2) + (h & 1) * 32 : half * HALF + h * 32;
+}
 
 // Element values of `E` per 16-byte chunk.
 template <bool F32>
@@ -400,23 +424,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tile < 0) break;
         const TilePos tp = locate(p, tile);
         const Job& jb = p.job[tp.job];
-        if (!wait_bar(ptx::smem_addr(&ctl->tempty[acc]), aph ^ 1u, abort_flag, p.err)) {
-          ok = false;
-          break;
+        const int steps = steps_of<F32>(jb.nkb, jb.pairs), per_pair = steps / jb.pairs;
+        for (int st = 0; ok && st < steps; ++st) {
+          const int blocks =
+              F32 ? 6 * min(F32_STEP, jb.nkb - (st % per_pair) * F32_STEP) : jb.nkb * jb.pairs;
+          if (!wait_bar(ptx::smem_addr(&ctl->tempty[acc]), aph ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * TILE;
+          if constexpr (MODE == FFN_GRADS) {
+            if (jb.mn) ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
+            else ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
+          } else {
+            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
+          }
+          if (!ok) break;
+          ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), 0x3);
+          acc ^= 1;
+          if (acc == 0) aph ^= 1u;
         }
-        ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * TILE;
-        const int blocks = jb.nkb * jb.pairs * (F32 ? 6 : 1);
-        if constexpr (MODE == FFN_GRADS) {
-          if (jb.mn) ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
-          else ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
-        } else {
-          ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
-        }
-        if (!ok) break;
-        ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), 0x3);
-        acc ^= 1;
-        if (acc == 0) aph ^= 1u;
       }
       if (!ok) {
         // Make sure no MMA is still writing TMEM before it is released.
@@ -447,8 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const TilePos tp = locate(p, tile);
       const Job& jb = p.job[tp.job];
       const CUtensorMap* mC = &maps.c[tp.job];
-      const uint32_t tempty_local = ptx::smem_addr(&ctl->tempty[acc]);
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE;
+      const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
       const int col0 = tp.tn * COLS + half * (COLS / 2);
       // R or D of a unit into the box, once the store before it has been read
@@ -461,8 +488,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         in_flight = true;
       };
       if (has_d && col0 < jb.c_cols) fetch(col0);
-      if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) break;
+      // hand the accumulator back to the MMA issuer (in the pair's first CTA)
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tempty[acc]), 0));
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+      };
+      if (F32) {
+        // sum the steps' accumulators; the total goes back into the last one's columns
+        const int steps = steps_of<F32>(jb.nkb, jb.pairs);
+        if (steps > 1) {
+          float sum[4][32];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) sum[i >> 5][i & 31] = 0.f;
+#pragma unroll 1
+          for (int st = 0; st < steps; ++st) {
+            if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) { ok = false; break; }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+              ptx::tmem_add16(lanes + acc * TILE + half_col<GATED>(half, h >> 1) + (h & 1) * 16,
+                              &sum[h >> 1][(h & 1) * 16]);
+            if (st + 1 < steps) release();
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            ptx::tmem_store32(lanes + acc * TILE + half_col<GATED>(half, h), sum[h]);
+        }
+      }
+      if (!(F32 && steps_of<F32>(jb.nkb, jb.pairs) > 1) &&
+          !wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err))
+        break;
       ptx::tc_fence_after();
+      const uint32_t tbase = lanes + acc * TILE;
 #pragma unroll 1
       for (int un = 0; un < UNITS; ++un) {
         const int col = col0 + un * UC;
@@ -532,12 +594,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) break;
-      // hand the accumulator back to the MMA issuer (in the pair's first CTA)
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_local, 0));
-      acc ^= 1;
-      if (acc == 0) aph ^= 1u;
+      release();
     }
     if (in_flight) wait_bar_drain(box_bar, box_ph, 100000000ull);
     if (lane == 0) ptx::bulk_wait<0>();  // this warp's output stores have landed

@@ -10,8 +10,6 @@ in a ``torch.autograd.Function``.  Likewise the feed-forward operators (``lce_li
 
 from __future__ import annotations
 
-import contextlib
-import ctypes
 from typing import Optional, Sequence
 
 import torch
@@ -255,77 +253,39 @@ def _activation(name: str) -> int:
     return _lib.ACTIVATIONS[name]
 
 
-def _rows(t: torch.Tensor, name: str, n: int, width: int, like: torch.Tensor) -> int:
-    """Checks a [n, width] matrix with unit column stride; returns its row stride."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of X")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must have the dtype of X ({like.dtype}), got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
-        raise ValueError(f"expected {name} [{n}, {width}], got {tuple(t.shape)}")
-    if n <= 1 and (width <= 1 or t.stride(1) == 1):
-        return width
-    if (width > 1 and t.stride(1) != 1) or t.stride(0) < width:
-        raise ValueError(f"{name} must have contiguous, non-overlapping rows (strides {t.stride()})")
-    return t.stride(0)
+# The calls below are made once per layer and token, where the host's time is the call's time: the
+# checks of tensors, the allocations and the C call are in the native binding (csrc/py_binding.cpp).
+
+def _call(what: str, name: str, stream: Optional[torch.cuda.Stream], *args):
+    """native.<name>(*args) on the current stream, or with ``stream`` made current: then what is
+    allocated inside belongs to the stream that the call's kernels run on."""
+    f = getattr(_lib.native(), name)
+    if stream is None:
+        r = f(*args)
+    else:
+        with torch.cuda.stream(stream):
+            r = f(*args)
+    if r.__class__ is int:
+        _lib.check(r, what)
+    return r
 
 
-def _dense(t: torch.Tensor, name: str, shape: tuple, like: torch.Tensor) -> None:
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of X")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must have the dtype of X ({like.dtype}), got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"expected {name} {list(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _check_x(X: torch.Tensor, W: torch.Tensor) -> str:
-    if not X.is_cuda:
-        raise ValueError("X must be a CUDA tensor")
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
-        raise ValueError(f"expected X [N, d] and W [width, d], got {tuple(X.shape)} and "
-                         f"{tuple(W.shape)}")
-    if X.dtype not in _DT:
-        raise TypeError(f"X and W must be bfloat16 or float32, got {X.dtype}")
-    return _DT[X.dtype]
-
-
-@contextlib.contextmanager
-def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
-    """The device, and the stream if one is given, made current: what is allocated inside belongs
-    to the stream that the call's kernels run on."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-def _workspace(size: int, what: str, workspace: Optional[torch.Tensor], dev) -> torch.Tensor:
-    if size == 0:
-        raise _lib.LceError(2, what)
-    if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=dev)
-    if workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    return workspace
+def _parts(parts: str):
+    if parts not in ("dx", "dw", "both"):
+        raise ValueError(f"parts must be 'dx', 'dw' or 'both', got {parts!r}")
+    return parts != "dw", parts != "dx"
 
 
 def lce_linear_workspace_size(N: int, d_in: int, d_out: int, activation: str = "none",
                               backward: bool = False, dtype: str = "bf16") -> int:
-    """Workspace bytes of lce_linear_forward / lce_linear_backward (0 when a shape rule is broken)."""
+    """Workspace bytes of lce_linear_forward / _backward (0 when a shape rule is broken)."""
     return int(_lib.load().lce_linear_workspace_size(N, d_in, d_out, _activation(activation),
                                                      int(backward), _lib.DTYPES[dtype]))
 
 
 def lce_gated_workspace_size(N: int, d: int, F: int, backward: bool = False,
                              dtype: str = "bf16") -> int:
-    """Workspace bytes of lce_gated_forward / lce_gated_backward (0 when a shape rule is broken)."""
+    """Workspace bytes of lce_gated_forward / _backward (0 when a shape rule is broken)."""
     return int(_lib.load().lce_gated_workspace_size(N, d, F, int(backward), _lib.DTYPES[dtype]))
 
 
@@ -336,26 +296,8 @@ def lce_linear_forward(X, W, bias=None, residual=None, *, activation: str = "non
     """Y = act(X W^T + bias) + residual.  X [N, d_in], residual and out [N, d_out] may have a row
     stride; W [d_out, d_in] and bias [d_out] are contiguous.  out may be residual itself.
     Returns (Y, workspace)."""
-    dt = _check_x(X, W)
-    N, d_in = X.shape
-    d_out = W.shape[0]
-    ldx = _rows(X, "X", N, d_in, X)
-    _dense(W, "W", (d_out, d_in), X)
-    if bias is not None:
-        _dense(bias, "bias", (d_out,), X)
-    ldr = _rows(residual, "residual", N, d_out, X) if residual is not None else 0
-    act = _activation(activation)
-    lib = _lib.load()
-    with _on(X.device, stream):
-        ws = _workspace(lib.lce_linear_workspace_size(N, d_in, d_out, act, 0, _lib.DTYPES[dt]),
-                        "lce_linear_workspace_size", workspace, X.device)
-        Y = torch.empty(N, d_out, dtype=X.dtype, device=X.device) if out is None else out
-        ldy = _rows(Y, "out", N, d_out, X)
-        st = lib.lce_linear_forward(_ptr(X), ldx, _ptr(W), _ptr(bias), _ptr(residual), ldr, N, d_in,
-                                    d_out, act, _lib.DTYPES[dt], _ptr(Y), ldy, _ptr(ws), ws.numel(),
-                                    _stream_handle(X.device, stream))
-    _lib.check(st, "lce_linear_forward")
-    return Y, ws
+    return _call("lce_linear_forward", "linear_forward", stream, X, W, bias, residual,
+                 _activation(activation), out, workspace)
 
 
 def lce_linear_backward(X, W, bias, dY, *, activation: str = "none", parts: str = "both",
@@ -364,29 +306,8 @@ def lce_linear_backward(X, W, bias, dY, *, activation: str = "none", parts: str 
     """Gradients of lce_linear_forward (the residual's is dY itself).  ``parts``: "dx", "dw"
     (weights and bias) or "both".  Returns (dX, dW, dbias, workspace); dbias is None without a
     bias, and what ``parts`` leaves out is None."""
-    if parts not in ("dx", "dw", "both"):
-        raise ValueError(f"parts must be 'dx', 'dw' or 'both', got {parts!r}")
-    dt = _check_x(X, W)
-    N, d_in = X.shape
-    d_out = W.shape[0]
-    ldx = _rows(X, "X", N, d_in, X)
-    _dense(W, "W", (d_out, d_in), X)
-    if bias is not None:
-        _dense(bias, "bias", (d_out,), X)
-    ldy = _rows(dY, "dY", N, d_out, X)
-    act = _activation(activation)
-    lib = _lib.load()
-    with _on(X.device, stream):
-        ws = _workspace(lib.lce_linear_workspace_size(N, d_in, d_out, act, 1, _lib.DTYPES[dt]),
-                        "lce_linear_workspace_size", workspace, X.device)
-        dX = torch.empty(N, d_in, dtype=X.dtype, device=X.device) if parts != "dw" else None
-        dW = torch.empty_like(W) if parts != "dx" else None
-        db = torch.empty_like(bias) if parts != "dx" and bias is not None else None
-        st = lib.lce_linear_backward(_ptr(X), ldx, _ptr(W), _ptr(bias), _ptr(dY), ldy, N, d_in, d_out,
-                                     act, _lib.DTYPES[dt], _ptr(dX), _ptr(dW), _ptr(db), _ptr(ws),
-                                     ws.numel(), _stream_handle(X.device, stream))
-    _lib.check(st, "lce_linear_backward")
-    return dX, dW, db, ws
+    return _call("lce_linear_backward", "linear_backward", stream, X, W, bias, dY,
+                 _activation(activation), *_parts(parts), workspace)
 
 
 def lce_gated_forward(X, Wg, Wu, *, activation: str = "silu", out: Optional[torch.Tensor] = None,
@@ -394,24 +315,8 @@ def lce_gated_forward(X, Wg, Wu, *, activation: str = "silu", out: Optional[torc
                       stream: Optional[torch.cuda.Stream] = None):
     """H = act(X Wg^T) * (X Wu^T).  X [N, d] and out [N, F] may have a row stride; Wg and Wu [F, d]
     are contiguous.  Returns (H, workspace)."""
-    dt = _check_x(X, Wg)
-    N, d = X.shape
-    F = Wg.shape[0]
-    ldx = _rows(X, "X", N, d, X)
-    _dense(Wg, "Wg", (F, d), X)
-    _dense(Wu, "Wu", (F, d), X)
-    act = _activation(activation)
-    lib = _lib.load()
-    with _on(X.device, stream):
-        ws = _workspace(lib.lce_gated_workspace_size(N, d, F, 0, _lib.DTYPES[dt]),
-                        "lce_gated_workspace_size", workspace, X.device)
-        H = torch.empty(N, F, dtype=X.dtype, device=X.device) if out is None else out
-        ldh = _rows(H, "out", N, F, X)
-        st = lib.lce_gated_forward(_ptr(X), ldx, _ptr(Wg), _ptr(Wu), N, d, F, act, _lib.DTYPES[dt],
-                                   _ptr(H), ldh, _ptr(ws), ws.numel(),
-                                   _stream_handle(X.device, stream))
-    _lib.check(st, "lce_gated_forward")
-    return H, ws
+    return _call("lce_gated_forward", "gated_forward", stream, X, Wg, Wu, _activation(activation),
+                 out, workspace)
 
 
 def lce_gated_backward(X, Wg, Wu, dH, *, activation: str = "silu", parts: str = "both",
@@ -419,28 +324,8 @@ def lce_gated_backward(X, Wg, Wu, dH, *, activation: str = "silu", parts: str = 
                        stream: Optional[torch.cuda.Stream] = None):
     """Gradients of lce_gated_forward.  ``parts``: "dx", "dw" (both weights) or "both".  Returns
     (dX, dWg, dWu, workspace); what ``parts`` leaves out is None."""
-    if parts not in ("dx", "dw", "both"):
-        raise ValueError(f"parts must be 'dx', 'dw' or 'both', got {parts!r}")
-    dt = _check_x(X, Wg)
-    N, d = X.shape
-    F = Wg.shape[0]
-    ldx = _rows(X, "X", N, d, X)
-    _dense(Wg, "Wg", (F, d), X)
-    _dense(Wu, "Wu", (F, d), X)
-    ldh = _rows(dH, "dH", N, F, X)
-    act = _activation(activation)
-    lib = _lib.load()
-    with _on(X.device, stream):
-        ws = _workspace(lib.lce_gated_workspace_size(N, d, F, 1, _lib.DTYPES[dt]),
-                        "lce_gated_workspace_size", workspace, X.device)
-        dX = torch.empty(N, d, dtype=X.dtype, device=X.device) if parts != "dw" else None
-        dWg = torch.empty_like(Wg) if parts != "dx" else None
-        dWu = torch.empty_like(Wu) if parts != "dx" else None
-        st = lib.lce_gated_backward(_ptr(X), ldx, _ptr(Wg), _ptr(Wu), _ptr(dH), ldh, N, d, F, act,
-                                    _lib.DTYPES[dt], _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(ws),
-                                    ws.numel(), _stream_handle(X.device, stream))
-    _lib.check(st, "lce_gated_backward")
-    return dX, dWg, dWu, ws
+    return _call("lce_gated_backward", "gated_backward", stream, X, Wg, Wu, dH,
+                 _activation(activation), *_parts(parts), workspace)
 
 
 def _as_rows(t: torch.Tensor, width: int) -> torch.Tensor:
@@ -483,7 +368,8 @@ class LinearAct(torch.autograd.Function):
             dx, dw, db, _ = lce_linear_backward(m, W, bias, _as_rows(dy, W.shape[0]),
                                                 activation=activation, parts=parts)
         return (None if dx is None else dx.view(shape), dw if ctx.needs_input_grad[1] else None,
-                db if ctx.needs_input_grad[2] else None, dy if ctx.needs_input_grad[3] else None, None)
+                db if ctx.needs_input_grad[2] else None,
+                dy if ctx.needs_input_grad[3] else None, None)
 
 
 class GatedLinear(torch.autograd.Function):
@@ -538,50 +424,6 @@ def gated_linear(x, Wg, Wu, activation: str = "silu"):
 
 # ------------------------------------------------------------------- gradient norm and clipping
 
-def _is_dense(t: torch.Tensor) -> bool:
-    """Whether t's elements fill one block of memory, in whatever order of its dimensions."""
-    if t.is_contiguous():
-        return True
-    step = 1
-    for stride, size in sorted(zip(t.stride(), t.shape)):
-        if size > 1:
-            if stride != step:
-                return False
-            step *= size
-    return True
-
-
-def _grad_table(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]]):
-    n = len(grads)
-    dev = None
-    dtypes = []
-    for t in grads:
-        if not t.is_cuda:
-            raise ValueError("gradients must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("gradients must be on one device")
-        name = _DT.get(t.dtype)
-        if name is None:
-            raise TypeError(f"gradients must be bfloat16 or float32, got {t.dtype}")
-        if not _is_dense(t):
-            raise ValueError(f"gradients must be dense (strides {t.stride()} of {tuple(t.shape)})")
-        dtypes.append(_lib.DTYPES[name])
-    outs = None
-    if out is not None:
-        if len(out) != n:
-            raise ValueError(f"{n} gradients and {len(out)} outputs")
-        for t, o in zip(grads, out):
-            if o.dtype != t.dtype or o.shape != t.shape or o.device != t.device or \
-                    (o.stride() != t.stride() and t.numel() > 1):
-                raise ValueError("each output must have its gradient's dtype, shape, strides and "
-                                 "device")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
-    return (dev, (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads]), outs,
-            (ctypes.c_int64 * n)(*[t.numel() for t in grads]), (ctypes.c_int32 * n)(*dtypes))
-
-
 def _norm(name: str) -> int:
     if name not in _lib.NORMS:
         raise ValueError(f"norm must be one of {sorted(_lib.NORMS)}, got {name!r}")
@@ -593,19 +435,7 @@ def lce_grad_norm(grads: Sequence[torch.Tensor], *, norm: str = "l2",
                   stream: Optional[torch.cuda.Stream] = None):
     """Global norm ("l2" or "inf") of a non-empty list of gradients (bfloat16 and float32 mixed,
     each dense).  Returns (total [] fp32 on the device, workspace)."""
-    if len(grads) == 0:
-        raise ValueError("no gradients")
-    kind = _norm(norm)
-    dev, ptrs, _, numels, dtypes = _grad_table(grads, None)
-    lib = _lib.load()
-    with _on(dev, stream):
-        ws = _workspace(lib.lce_grad_norm_workspace_size(len(grads)), "lce_grad_norm_workspace_size",
-                        workspace, dev)
-        total = torch.empty((), dtype=torch.float32, device=dev)
-        st = lib.lce_grad_norm(ptrs, numels, dtypes, len(grads), kind, _ptr(total), _ptr(ws),
-                               ws.numel(), _stream_handle(dev, stream))
-    _lib.check(st, "lce_grad_norm")
-    return total, ws
+    return _call("lce_grad_norm", "clip", stream, grads, None, _norm(norm), None, workspace)
 
 
 def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: str = "l2",
@@ -615,20 +445,12 @@ def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: 
     """Scales a non-empty list of gradients by min(1, max_norm / (total + 1e-6)), total their global
     norm: in place, or into ``out`` (tensors of the same dtypes, shapes and strides).  Nothing is
     read back to the host.  Returns (total [] fp32 on the device, the scaled tensors, workspace)."""
-    if len(grads) == 0:
-        raise ValueError("no gradients")
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
-    kind = _norm(norm)
-    dev, ptrs, outs, numels, dtypes = _grad_table(grads, out)
-    lib = _lib.load()
-    with _on(dev, stream):
-        ws = _workspace(lib.lce_grad_norm_workspace_size(len(grads)), "lce_grad_norm_workspace_size",
-                        workspace, dev)
-        total = torch.empty((), dtype=torch.float32, device=dev)
-        st = lib.lce_clip_grad_norm(ptrs, outs, numels, dtypes, len(grads), kind, float(max_norm),
-                                    _ptr(total), _ptr(ws), ws.numel(), _stream_handle(dev, stream))
-    _lib.check(st, "lce_clip_grad_norm")
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
+    total, ws = _call("lce_clip_grad_norm", "clip", stream, grads, out, _norm(norm),
+                      float(max_norm), workspace)
     return total, list(grads if out is None else out), ws
 
 

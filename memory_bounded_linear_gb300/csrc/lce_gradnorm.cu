@@ -3,19 +3,20 @@
 //   total = sqrt(sum over arrays of sum of g^2)   (or max |g|),   c = min(1, max_norm / (total + 1e-6))
 //   out   = g c
 //
-// Two launches.  The first cuts the arrays into chunks of CHUNK elements and gives block b the chunks
-// b, b + grid, ...; each block writes one partial.  The second reads all partials (every block for
-// itself, in the same order), forms c and scales its chunks.  The table of the arrays is a kernel
-// argument, so nothing is copied to the device and a captured graph holds its own table; lists
-// longer than one table take several launches of each kind.
-// Both passes are bound by memory: 2 x the arrays' bytes are read (the second time from L2 as far
-// as they fit) and once written.
+// Two launches.  The first cuts the arrays into chunks (up to 64 KB, smaller where that would leave
+// SMs without one) and gives block b the chunks b, b + grid, ...; each block writes one partial.  The
+// second reads all partials (every block for itself, in the same order), forms c and scales the
+// chunks, last one first, so that what the first pass left in L2 is not read from memory again.  The
+// table of the arrays is a kernel argument: nothing is copied to the device, and a captured graph
+// holds its own table; lists longer than one table take several launches of each kind.
+// Both passes are bound by memory: the arrays are read twice and written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lce.h"
 #include "lce_internal.h"
@@ -23,21 +24,25 @@
 namespace lce {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int64_t CHUNK = 16384;       // elements: 64 per thread
-constexpr int TABLE = 512;             // arrays per launch
-constexpr int MAX_BLOCKS = 152 * 4;    // blocks of one norm launch
+constexpr int THREADS = 512;
+constexpr int UNROLL = 8;              // 16-byte vectors a thread has in flight
+constexpr int TABLE = 512;             // arrays per launch,
+constexpr int SMALL_TABLE = 40;        // or, for a short list, a table of 1.3 KB instead of 17
+constexpr int MAX_BLOCKS = 152 * 2;    // blocks of one launch: 1,024 threads per SM
 
+template <int CAP>
 struct Table {
-  const void* in[TABLE];
-  void* out[TABLE];
-  int64_t numel[TABLE];
-  int64_t first[TABLE + 1];  // first chunk of each array
-  unsigned char f32[TABLE];
+  const void* in[CAP];
+  void* out[CAP];
+  int64_t numel[CAP];
+  int64_t first[CAP + 1];  // first chunk of each array
+  unsigned char f32[CAP];
   int count;
+  int vectors;               // 16-byte vectors per chunk: THREADS x 1, 2, 4 or 8
 };
 
-__device__ __forceinline__ int find(const Table& t, int64_t chunk) {
+template <int CAP>
+__device__ __forceinline__ int find(const Table<CAP>& t, int64_t chunk) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -51,7 +56,7 @@ __device__ __forceinline__ int find(const Table& t, int64_t chunk) {
 __device__ __forceinline__ unsigned mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 struct Acc {
-  float s;     // sum of squares of at most CHUNK / THREADS values
+  float s;     // sum of squares of at most 64 values (and up to 14 at the unaligned ends)
   unsigned m;  // largest magnitude
   template <bool INF>
   __device__ __forceinline__ void add(float x) {
@@ -60,54 +65,115 @@ struct Acc {
   }
 };
 
-template <typename E, bool INF>
-__device__ __forceinline__ void visit(const E* p, int64_t n, Acc& a) {
-  for (int64_t i = threadIdx.x; i < n; i += THREADS) a.add<INF>(static_cast<float>(p[i]));
+template <typename E>
+constexpr int PER_VEC = 16 / sizeof(E);
+
+template <typename E>
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[PER_VEC<E>]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 2) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
 }
 
+// Elements before the first 16-byte boundary of p.
+template <typename E>
+__device__ __forceinline__ int head_of(const E* p, int64_t n) {
+  const int h = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) /
+                static_cast<int>(sizeof(E));
+  return static_cast<int>(min(static_cast<int64_t>(h), n));
+}
+
+template <typename E, bool INF>
+__device__ __forceinline__ void visit(const E* p, int64_t n, Acc& a) {
+  const int head = head_of(p, n);
+  const int nvec = static_cast<int>((n - head) / PER_VEC<E>);
+  const int tail = static_cast<int>(n - head) - nvec * PER_VEC<E>;
+  const uint4* v = reinterpret_cast<const uint4*>(p + head);
+  uint4 q[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const int i = threadIdx.x + u * THREADS;
+    q[u] = i < nvec ? v[i] : make_uint4(0, 0, 0, 0);
+  }
+  if (threadIdx.x < head) a.add<INF>(static_cast<float>(p[threadIdx.x]));
+  if (threadIdx.x < tail) a.add<INF>(static_cast<float>(p[n - tail + threadIdx.x]));
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    float f[PER_VEC<E>];
+    unpack<E>(q[u], f);
+#pragma unroll
+    for (int i = 0; i < PER_VEC<E>; ++i) a.add<INF>(f[i]);
+  }
+}
+
+// The block's sum (or maximum) of v in a fixed order, in thread 0.
 template <bool INF>
-__global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ Table t, double* part) {
+__device__ __forceinline__ double reduce(double v) {
+  __shared__ double sh[THREADS / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = INF ? fmax(v, w) : v + w;
+  }
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < THREADS / 32; ++i) v = INF ? fmax(v, sh[i]) : v + sh[i];
+  }
+  return v;
+}
+
+// A chunk of the table: its array and its elements.
+struct Chunk {
+  int k;
+  int64_t i0, n;
+};
+template <int CAP>
+__device__ __forceinline__ Chunk chunk_of(const Table<CAP>& t, int64_t c) {
+  Chunk r;
+  r.k = find(t, c);
+  const int64_t size = static_cast<int64_t>(t.vectors) * (t.f32[r.k] ? 4 : 8);
+  r.i0 = (c - t.first[r.k]) * size;
+  r.n = min(size, t.numel[r.k] - r.i0);
+  return r;
+}
+
+template <bool INF, int CAP>
+__global__ void __launch_bounds__(THREADS, 2)
+    norm_kernel(const __grid_constant__ Table<CAP> t, double* part) {
   double sum = 0.0;
   unsigned m = 0;
   for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = find(t, c);
-    const int64_t i0 = (c - t.first[k]) * CHUNK;
-    const int64_t n = min(CHUNK, t.numel[k] - i0);
+    const Chunk ch = chunk_of(t, c);
     Acc a{0.f, 0u};
-    if (t.f32[k]) visit<float, INF>(static_cast<const float*>(t.in[k]) + i0, n, a);
-    else visit<__nv_bfloat16, INF>(static_cast<const __nv_bfloat16*>(t.in[k]) + i0, n, a);
+    if (t.f32[ch.k]) visit<float, INF>(static_cast<const float*>(t.in[ch.k]) + ch.i0, ch.n, a);
+    else visit<__nv_bfloat16, INF>(static_cast<const __nv_bfloat16*>(t.in[ch.k]) + ch.i0, ch.n, a);
     sum += static_cast<double>(a.s);
     m = max(m, a.m);
   }
-  __shared__ double sh[THREADS];
-  sh[threadIdx.x] = INF ? static_cast<double>(m) : sum;
-  __syncthreads();
-  for (int w = THREADS / 2; w > 0; w >>= 1) {
-    if (threadIdx.x < w) {
-      const double o = sh[threadIdx.x + w];
-      sh[threadIdx.x] = INF ? fmax(sh[threadIdx.x], o) : sh[threadIdx.x] + o;
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[blockIdx.x] = sh[0];
+  const double r = reduce<INF>(INF ? static_cast<double>(m) : sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
 
 // The total from all partials: the same sum, in the same order, whichever block computes it.
 template <bool INF>
-__device__ float total_of(const double* part, int parts) {
-  __shared__ double sh[THREADS];
+__device__ __forceinline__ float total_of(const double* part, int parts) {
+  __shared__ float total;
   double v = 0.0;
   for (int i = threadIdx.x; i < parts; i += THREADS) v = INF ? fmax(v, part[i]) : v + part[i];
-  sh[threadIdx.x] = v;
+  v = reduce<INF>(v);
+  if (threadIdx.x == 0)
+    total = INF ? __uint_as_float(static_cast<unsigned>(v)) : static_cast<float>(sqrt(v));
   __syncthreads();
-  for (int w = THREADS / 2; w > 0; w >>= 1) {
-    if (threadIdx.x < w) {
-      const double o = sh[threadIdx.x + w];
-      sh[threadIdx.x] = INF ? fmax(sh[threadIdx.x], o) : sh[threadIdx.x] + o;
-    }
-    __syncthreads();
-  }
-  return INF ? __uint_as_float(static_cast<unsigned>(sh[0])) : static_cast<float>(sqrt(sh[0]));
+  return total;
 }
 
 template <bool INF>
@@ -117,49 +183,92 @@ __global__ void __launch_bounds__(THREADS) total_kernel(const double* part, int 
 }
 
 template <typename E>
-__device__ __forceinline__ void scale(const E* in, E* out, int64_t n, float c) {
-  for (int64_t i = threadIdx.x; i < n; i += THREADS)
-    out[i] = static_cast<E>(static_cast<float>(in[i]) * c);
+__device__ __forceinline__ E scaled(E x, float c) {
+  return static_cast<E>(static_cast<float>(x) * c);
 }
 
-template <bool INF>
-__global__ void __launch_bounds__(THREADS)
-    scale_kernel(const __grid_constant__ Table t, const double* part, int parts, float max_norm,
+template <typename E>
+__device__ __forceinline__ void scale(const E* in, E* out, int64_t n, float c) {
+  if ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
+    // the two are never 16-byte aligned together
+    for (int i = threadIdx.x; i < n; i += THREADS) out[i] = scaled(in[i], c);
+    return;
+  }
+  const int head = head_of(in, n);
+  const int nvec = static_cast<int>((n - head) / PER_VEC<E>);
+  const int tail = static_cast<int>(n - head) - nvec * PER_VEC<E>;
+  const uint4* v = reinterpret_cast<const uint4*>(in + head);
+  uint4* o = reinterpret_cast<uint4*>(out + head);
+  uint4 q[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const int i = threadIdx.x + u * THREADS;
+    q[u] = i < nvec ? __ldcs(v + i) : make_uint4(0, 0, 0, 0);  // the last use of these values
+  }
+  if (threadIdx.x < head) out[threadIdx.x] = scaled(in[threadIdx.x], c);
+  if (threadIdx.x < tail) out[n - tail + threadIdx.x] = scaled(in[n - tail + threadIdx.x], c);
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    float f[PER_VEC<E>];
+    unpack<E>(q[u], f);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(E) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j] * c, f[2 * j + 1] * c);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[j] = __float_as_uint(f[j] * c);
+      }
+    }
+    const int i = threadIdx.x + u * THREADS;
+    if (i < nvec) __stcs(o + i, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
+template <bool INF, int CAP>
+__global__ void __launch_bounds__(THREADS, 2)
+    scale_kernel(const __grid_constant__ Table<CAP> t, const double* part, int parts, float max_norm,
                  float* total) {
   const float v = total_of<INF>(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *total = v;
   const float q = max_norm / (v + 1e-6f);
   const float c = q > 1.f ? 1.f : q;  // NaN stays
-  for (int64_t ch = blockIdx.x; ch < t.first[t.count]; ch += gridDim.x) {
-    const int k = find(t, ch);
-    if (c == 1.f && t.in[k] == t.out[k]) continue;
-    const int64_t i0 = (ch - t.first[k]) * CHUNK;
-    const int64_t n = min(CHUNK, t.numel[k] - i0);
-    if (t.f32[k])
-      scale(static_cast<const float*>(t.in[k]) + i0, static_cast<float*>(t.out[k]) + i0, n, c);
+  for (int64_t i = t.first[t.count] - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
+    const Chunk ch = chunk_of(t, i);
+    if (c == 1.f && t.in[ch.k] == t.out[ch.k]) continue;
+    if (t.f32[ch.k])
+      scale(static_cast<const float*>(t.in[ch.k]) + ch.i0, static_cast<float*>(t.out[ch.k]) + ch.i0,
+            ch.n, c);
     else
-      scale(static_cast<const __nv_bfloat16*>(t.in[k]) + i0,
-            static_cast<__nv_bfloat16*>(t.out[k]) + i0, n, c);
+      scale(static_cast<const __nv_bfloat16*>(t.in[ch.k]) + ch.i0,
+            static_cast<__nv_bfloat16*>(t.out[ch.k]) + ch.i0, ch.n, c);
   }
 }
 
 // Calls f(table) for the list cut into tables; empty arrays are left out.
-template <typename F>
+template <int CAP, typename F>
 cudaError_t for_tables(const void* const* grads, void* const* out, const int64_t* numels,
                        const int32_t* dtypes, int64_t count, F&& f) {
-  Table t;
+  double bytes = 0.0;
+  for (int64_t i = 0; i < count; ++i)
+    bytes += static_cast<double>(numels[i]) * (dtypes[i] == LCE_F32 ? 4 : 2);
+  Table<CAP> t;
+  t.vectors = THREADS;
+  while (t.vectors < THREADS * UNROLL && bytes > 16.0 * t.vectors * MAX_BLOCKS) t.vectors *= 2;
   t.count = 0;
   t.first[0] = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (numels[i] > 0) {
       const int k = t.count++;
+      const int64_t size = static_cast<int64_t>(t.vectors) * (dtypes[i] == LCE_F32 ? 4 : 8);
       t.in[k] = grads[i];
       t.out[k] = out ? out[i] : const_cast<void*>(grads[i]);
       t.numel[k] = numels[i];
       t.f32[k] = dtypes[i] == LCE_F32;
-      t.first[k + 1] = t.first[k] + (numels[i] + CHUNK - 1) / CHUNK;
+      t.first[k + 1] = t.first[k] + (numels[i] + size - 1) / size;
     }
-    if (t.count == TABLE || (i + 1 == count && t.count > 0)) {
+    if (t.count == CAP || (i + 1 == count && t.count > 0)) {
       cudaError_t e = f(t);
       if (e != cudaSuccess) return e;
       t.count = 0;
@@ -192,16 +301,16 @@ lce_status_t checks(const void* const* grads, void* const* out, const int64_t* n
   return LCE_OK;
 }
 
-template <bool INF>
+template <bool INF, int CAP>
 lce_status_t run(const void* const* grads, void* const* out, const int64_t* numels,
                  const int32_t* dtypes, int64_t count, bool clip, float max_norm, float* total,
                  void* workspace, cudaStream_t stream) {
   double* part = reinterpret_cast<double*>(static_cast<char*>(workspace) + WS_HEADER_BYTES);
   int parts = 0;
-  cudaError_t e = for_tables(grads, out, numels, dtypes, count, [&](const Table& t) {
+  cudaError_t e = for_tables<CAP>(grads, out, numels, dtypes, count, [&](const Table<CAP>& t) {
     const int blocks = static_cast<int>(std::min<int64_t>(t.first[t.count], MAX_BLOCKS));
     const cudaError_t r = traced(K_GRAD_NORM, stream, [&] {
-      norm_kernel<INF><<<blocks, THREADS, 0, stream>>>(t, part + parts);
+      norm_kernel<INF, CAP><<<blocks, THREADS, 0, stream>>>(t, part + parts);
       return cudaGetLastError();
     });
     parts += blocks;
@@ -215,10 +324,10 @@ lce_status_t run(const void* const* grads, void* const* out, const int64_t* nume
     });
     return e == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
   }
-  e = for_tables(grads, out, numels, dtypes, count, [&](const Table& t) {
+  e = for_tables<CAP>(grads, out, numels, dtypes, count, [&](const Table<CAP>& t) {
     const int blocks = static_cast<int>(std::min<int64_t>(t.first[t.count], MAX_BLOCKS));
     return traced(K_GRAD_SCALE, stream, [&] {
-      scale_kernel<INF><<<blocks, THREADS, 0, stream>>>(t, part, parts, max_norm, total);
+      scale_kernel<INF, CAP><<<blocks, THREADS, 0, stream>>>(t, part, parts, max_norm, total);
       return cudaGetLastError();
     });
   });
@@ -234,9 +343,15 @@ lce_status_t entry(const void* const* grads, void* const* out, const int64_t* nu
   int num_sms = 0;
   if ((st = check_device(&num_sms)) != LCE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return norm == LCE_NORM_INF
-             ? run<true>(grads, out, numels, dtypes, count, clip, max_norm, total, workspace, s)
-             : run<false>(grads, out, numels, dtypes, count, clip, max_norm, total, workspace, s);
+  auto go = [&](auto inf) {
+    constexpr bool INF = decltype(inf)::value;
+    return count <= SMALL_TABLE
+               ? run<INF, SMALL_TABLE>(grads, out, numels, dtypes, count, clip, max_norm, total,
+                                       workspace, s)
+               : run<INF, TABLE>(grads, out, numels, dtypes, count, clip, max_norm, total, workspace,
+                                 s);
+  };
+  return norm == LCE_NORM_INF ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace

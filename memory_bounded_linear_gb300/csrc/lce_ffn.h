@@ -57,12 +57,27 @@ struct FfnTc {
   int64_t part_stride;
 };
 
-// Tensor cores: lce_ffn_tc.cu.  Several jobs only for FFN_GRADS; header: the workspace header.
+// What is known to be zero in the workspace header when a launch is made; a launch updates it.
+struct HeaderState {
+  bool flags = false;  // the error flags
+  bool sched = false;  // the scheduler counters
+};
+
+// Tensor cores: lce_ffn_tc.cu.  Several jobs only for FFN_GRADS, where a job whose C is null is not
+// computed but counted when the launch is planned; header: the workspace header.
 cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
-                          int num_sms, cudaStream_t stream);
-// fp32 x [rows x cols], row stride ld, into three bf16 parts of row stride ld_out: lce_ffn_simt.cu
-cudaError_t launch_split_bf16(const float* x, int64_t ld, int64_t rows, int64_t cols, void* out,
-                              int64_t ld_out, int64_t part_stride, cudaStream_t stream);
+                          HeaderState* state, int num_sms, cudaStream_t stream);
+// fp32 x [rows x cols], row stride ld, into three bf16 parts of row stride ld_out, part_stride
+// apart, for several arrays; clears the workspace header: lce_ffn_simt.cu
+struct SplitArray {
+  const float* x;
+  int64_t ld, rows, cols;
+  void* out;
+  int64_t ld_out, part_stride;
+};
+constexpr int MAX_SPLIT_ARRAYS = 3;
+cudaError_t launch_split_bf16(const SplitArray* arrays, int count, unsigned* header,
+                              cudaStream_t stream);
 // Few tokens, bf16 (at most FFN_FEW_TOKENS rows): lce_ffn_few.cu.  Clears the error flags.
 constexpr int64_t FFN_FEW_TOKENS = 128;
 cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream);

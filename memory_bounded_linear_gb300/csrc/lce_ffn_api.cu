@@ -86,31 +86,34 @@ struct Call {
   char* ws;
   int num_sms;
   cudaStream_t stream;
+  HeaderState header{};
+  SplitArray split[MAX_SPLIT_ARRAYS];
+  int nsplit = 0;
 
-  cudaError_t few(int kid, const FfnGemm& g) const {
+  unsigned* flags() const { return reinterpret_cast<unsigned*>(ws); }
+  cudaError_t few(int kid, const FfnGemm& g) {
     return traced(kid, stream, [&] {
-      unsigned* err = reinterpret_cast<unsigned*>(ws);
-      return dt == LCE_BF16 ? launch_ffn_few(g, err, num_sms, stream)
-                            : launch_ffn_few_f32(g, err, stream);
+      return dt == LCE_BF16 ? launch_ffn_few(g, flags(), num_sms, stream)
+                            : launch_ffn_few_f32(g, flags(), stream);
     });
   }
-  cudaError_t tc(int kid, const FfnTc* jobs, int n) const {
-    return traced(kid, stream, [&] {
-      return launch_ffn_tc(jobs, n, dt, reinterpret_cast<unsigned*>(ws), num_sms, stream);
-    });
+  cudaError_t tc(int kid, const FfnTc* jobs, int n) {
+    return traced(kid, stream,
+                  [&] { return launch_ffn_tc(jobs, n, dt, flags(), &header, num_sms, stream); });
   }
-  // x [rows x cols] as an operand of the tensor-core kernel: itself, or its parts in slot s
-  cudaError_t operand(const void* x, int64_t ld, int64_t rows, int64_t cols, const Slot& s,
-                      FfnOperand* o) const {
-    if (dt == LCE_BF16) {
-      *o = FfnOperand{x, rows, cols, ld, 1, 0};
-      return cudaSuccess;
-    }
-    *o = parts(s, rows, cols);
-    return traced(K_SPLIT_BF16, stream, [&] {
-      return launch_split_bf16(static_cast<const float*>(x), ld, rows, cols, ws + s.off, s.ld,
-                               s.part_stride, stream);
-    });
+  // x [rows x cols] as an operand of the tensor-core kernel: itself, or its parts in slot s, which
+  // the next split_all() writes
+  FfnOperand operand(const void* x, int64_t ld, int64_t rows, int64_t cols, const Slot& s) {
+    if (dt == LCE_BF16) return FfnOperand{x, rows, cols, ld, 1, 0};
+    split[nsplit++] = SplitArray{static_cast<const float*>(x), ld, rows, cols, ws + s.off, s.ld,
+                                 s.part_stride};
+    return parts(s, rows, cols);
+  }
+  cudaError_t split_all() {
+    if (nsplit == 0) return cudaSuccess;
+    header.flags = header.sched = true;  // the launch clears the header
+    return traced(K_SPLIT_BF16, stream,
+                  [&] { return launch_split_bf16(split, nsplit, flags(), stream); });
   }
   // an array of the workspace as an operand
   FfnOperand parts(const Slot& s, int64_t rows, int64_t cols) const {
@@ -120,31 +123,24 @@ struct Call {
 
 // dX = dZ W (+ dZ2 W2), dW = dZ^T X (and dW2 = dZ2^T X) in one launch, the longer sums first.
 // nw = 1 or 2 weights; dX or the dW may be null.
-cudaError_t products(const Call& c, const FfnOperand& X, const FfnOperand* W, const FfnOperand* Z,
+cudaError_t products(Call& c, const FfnOperand& X, const FfnOperand* W, const FfnOperand* Z,
                      int nw, int64_t N, int64_t d, int64_t width, void* dX, void* const* dW) {
+  if (!dX && !dW[0]) return cudaSuccess;
   FfnTc jobs[3];
-  int n = 0;
-  auto add_dx = [&] {
-    if (!dX) return;
-    FfnTc& g = jobs[n++] = FfnTc{};
-    g.M = N; g.Ncols = d; g.K = width;
-    g.A = Z[0]; g.B = W[0]; g.b_mn = true;
-    if (nw == 2) { g.A2 = Z[1]; g.B2 = W[1]; }
-    g.C = dX; g.ldc = d;
-  };
-  auto add_dw = [&] {
-    for (int i = 0; i < nw && dW[0]; ++i) {
-      FfnTc& g = jobs[n++] = FfnTc{};
-      g.M = width; g.Ncols = d; g.K = N;
-      g.A = Z[i]; g.B = X; g.a_mn = g.b_mn = true;
-      g.C = dW[i]; g.ldc = d;
-    }
-  };
-  if (nw * width >= N) { add_dx(); add_dw(); }
-  else { add_dw(); add_dx(); }
-  if (n == 0) return cudaSuccess;
-  for (int i = 0; i < n; ++i) { jobs[i].mode = FFN_GRADS; jobs[i].act = LCE_ACT_NONE; }
-  return c.tc(K_FFN_GRADS, jobs, n);
+  const bool dx_first = nw * width >= N;
+  FfnTc& x = jobs[dx_first ? 0 : nw] = FfnTc{};
+  x.M = N; x.Ncols = d; x.K = width;
+  x.A = Z[0]; x.B = W[0]; x.b_mn = true;
+  if (nw == 2) { x.A2 = Z[1]; x.B2 = W[1]; }
+  x.C = dX; x.ldc = d;
+  for (int i = 0; i < nw; ++i) {
+    FfnTc& w = jobs[dx_first ? i + 1 : i] = FfnTc{};
+    w.M = width; w.Ncols = d; w.K = N;
+    w.A = Z[i]; w.B = X; w.a_mn = w.b_mn = true;
+    w.C = dW[i]; w.ldc = d;
+  }
+  for (int i = 0; i <= nw; ++i) { jobs[i].mode = FFN_GRADS; jobs[i].act = LCE_ACT_NONE; }
+  return c.tc(K_FFN_GRADS, jobs, nw + 1);
 }
 
 }  // namespace
@@ -181,11 +177,9 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  // the kernels for a few tokens clear the error flags themselves
-  if ((N == 0 || !few_tokens(N, dtype)) && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess)
-    return LCE_ERR_CUDA;
-  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
-  if (N == 0) return LCE_OK;
+  if (N == 0)  // otherwise the first launch clears the error flags
+    return zero(workspace, WS_HEADER_BYTES, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   if (few_tokens(N, dtype)) {
     FfnGemm g{};
     g.mode = FFN_LINEAR;
@@ -203,10 +197,9 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   g.M = N; g.Ncols = d_out; g.K = d_in;
   g.bias = bias; g.R = residual; g.ldr = ldr;
   g.C = Y; g.ldc = ldy;
-  if (c.operand(X, ldx, N, d_in, L.x, &g.A) != cudaSuccess ||
-      c.operand(W, d_in, d_out, d_in, L.w[0], &g.B) != cudaSuccess ||
-      c.tc(K_LIN, &g, 1) != cudaSuccess)
-    return LCE_ERR_CUDA;
+  g.A = c.operand(X, ldx, N, d_in, L.x);
+  g.B = c.operand(W, d_in, d_out, d_in, L.w[0]);
+  if (c.split_all() != cudaSuccess || c.tc(K_LIN, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
   return LCE_OK;
 }
 
@@ -228,23 +221,22 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
   if (N == 0) {
+    if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
     const size_t e = elem(dtype);
     if (zero(dW, static_cast<size_t>(d_in) * d_out * e, stream) != cudaSuccess ||
         zero(dbias, static_cast<size_t>(d_out) * e, stream) != cudaSuccess)
       return LCE_ERR_CUDA;
     return LCE_OK;
   }
-  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   const Layout L = linear_layout(N, d_in, d_out, activation, true, dtype);
-  FfnOperand x, w, z;
-  if (c.operand(X, ldx, N, d_in, L.x, &x) != cudaSuccess ||
-      c.operand(W, d_in, d_out, d_in, L.w[0], &w) != cudaSuccess)
-    return LCE_ERR_CUDA;
-  if (activation == LCE_ACT_NONE) {
-    if (c.operand(dY, ldy, N, d_out, L.z[0], &z) != cudaSuccess) return LCE_ERR_CUDA;
-  } else {
+  const FfnOperand x = c.operand(X, ldx, N, d_in, L.x);
+  const FfnOperand w = c.operand(W, d_in, d_out, d_in, L.w[0]);
+  const bool none = activation == LCE_ACT_NONE;
+  const FfnOperand z = none ? c.operand(dY, ldy, N, d_out, L.z[0]) : c.parts(L.z[0], N, d_out);
+  if (c.split_all() != cudaSuccess) return LCE_ERR_CUDA;
+  if (!none) {
     FfnTc g{};
     g.mode = FFN_LINEAR_DZ;
     g.act = activation;
@@ -253,14 +245,16 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
     g.bias = bias; g.D = dY; g.ldd = ldy;
     g.C = c.ws + L.z[0].off; g.ldc = L.z[0].ld; g.part_stride = L.z[0].part_stride;
     if (c.tc(K_LIN_DZ, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
-    z = c.parts(L.z[0], N, d_out);
   }
   if (dbias && traced(K_COLSUM, stream, [&] {
         return launch_column_sum(z.ptr, z.ld, N, d_out, static_cast<int>(z.parts), z.part_stride,
                                  dbias, stream);
       }) != cudaSuccess)
     return LCE_ERR_CUDA;
-  return products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  if (products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) != cudaSuccess) return LCE_ERR_CUDA;
+  // no launch that clears the error flags (dbias alone, or nothing asked for)
+  if (!c.header.flags && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
+  return LCE_OK;
 }
 
 size_t lce_gated_workspace_size(int64_t N, int64_t d, int64_t F, int32_t backward,
@@ -287,11 +281,9 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  // the kernels for a few tokens clear the error flags themselves
-  if ((N == 0 || !few_tokens(N, dtype)) && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess)
-    return LCE_ERR_CUDA;
-  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
-  if (N == 0) return LCE_OK;
+  if (N == 0)  // otherwise the first launch clears the error flags
+    return zero(workspace, WS_HEADER_BYTES, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+  Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   if (few_tokens(N, dtype)) {
     FfnGemm g{};
     g.mode = FFN_GATED;
@@ -307,10 +299,10 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   g.act = activation;
   g.M = N; g.Ncols = F; g.K = d;
   g.C = H; g.ldc = ldh;
-  if (c.operand(X, ldx, N, d, L.x, &g.A) != cudaSuccess ||
-      c.operand(Wg, d, F, d, L.w[0], &g.B) != cudaSuccess ||
-      c.operand(Wu, d, F, d, L.w[1], &g.B2) != cudaSuccess || c.tc(K_GATED, &g, 1) != cudaSuccess)
-    return LCE_ERR_CUDA;
+  g.A = c.operand(X, ldx, N, d, L.x);
+  g.B = c.operand(Wg, d, F, d, L.w[0]);
+  g.B2 = c.operand(Wu, d, F, d, L.w[1]);
+  if (c.split_all() != cudaSuccess || c.tc(K_GATED, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
   return LCE_OK;
 }
 
@@ -332,20 +324,19 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
   lce_status_t st = check_device(&num_sms);
   if (st != LCE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
   if (N == 0) {
+    if (zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
     const size_t bytes = static_cast<size_t>(d) * F * elem(dtype);
     if (zero(dWg, bytes, stream) != cudaSuccess || zero(dWu, bytes, stream) != cudaSuccess)
       return LCE_ERR_CUDA;
     return LCE_OK;
   }
-  const Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
+  Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   const Layout L = gated_layout(N, d, F, true, dtype);
-  FfnOperand x, w[2], z[2];
-  if (c.operand(X, ldx, N, d, L.x, &x) != cudaSuccess ||
-      c.operand(Wg, d, F, d, L.w[0], &w[0]) != cudaSuccess ||
-      c.operand(Wu, d, F, d, L.w[1], &w[1]) != cudaSuccess)
-    return LCE_ERR_CUDA;
+  const FfnOperand x = c.operand(X, ldx, N, d, L.x);
+  const FfnOperand w[2] = {c.operand(Wg, d, F, d, L.w[0]), c.operand(Wu, d, F, d, L.w[1])};
+  const FfnOperand z[2] = {c.parts(L.z[0], N, F), c.parts(L.z[1], N, F)};
+  if (c.split_all() != cudaSuccess) return LCE_ERR_CUDA;
   FfnTc g{};
   g.mode = FFN_GATED_DGU;
   g.act = activation;
@@ -355,7 +346,6 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
   g.C = c.ws + L.z[0].off; g.C2 = c.ws + L.z[1].off;
   g.ldc = L.z[0].ld; g.part_stride = L.z[0].part_stride;
   if (c.tc(K_GATED_DGU, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
-  for (int i = 0; i < 2; ++i) z[i] = c.parts(L.z[i], N, F);
   void* const dW[2] = {dWg, dWu};
   return products(c, x, w, z, 2, N, d, F, dX, dW) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
 }

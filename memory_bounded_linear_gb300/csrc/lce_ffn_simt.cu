@@ -8,6 +8,7 @@
 #include "lce_act.cuh"
 #include "lce_ffn.h"
 #include "lce_internal.h"
+#include "ptx.cuh"
 
 namespace lce {
 namespace {
@@ -100,41 +101,129 @@ cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------- column sums
-// One thread per column, rows in order.
-template <typename E, int PARTS, typename O>
-__global__ void column_sum_kernel(const E* x, int64_t ld, int64_t part_stride, int64_t N, int64_t cols,
-                                  O* out) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.f;
-  for (int64_t r = 0; r < N; ++r) {
-    float v = 0.f;
-#pragma unroll
-    for (int k = PARTS - 1; k >= 0; --k) v += static_cast<float>(x[k * part_stride + r * ld + c]);
-    s += v;
-  }
-  out[c] = static_cast<O>(s);
+// Bound by reading x once.  A cluster of eight blocks takes a strip of 128 columns; warp w of block
+// r sums the rows 8 r + w, 64 + 8 r + w, ... (a row of the strip is 256 contiguous bytes, eight rows
+// in flight), the warps meet in shared memory and the blocks through distributed shared memory, in a
+// fixed order: one launch, no workspace, no atomics.
+constexpr int SUM_COLS = 128;
+constexpr int SUM_SPLIT = 8;
+constexpr int SUM_UNROLL = 8;
+
+__device__ __forceinline__ void add4(float (&s)[4], const uint2& q) {
+  s[0] += __uint_as_float(q.x << 16);
+  s[1] += __uint_as_float(q.x & 0xffff0000u);
+  s[2] += __uint_as_float(q.y << 16);
+  s[3] += __uint_as_float(q.y & 0xffff0000u);
 }
 
-// fp32 rows into bf16 parts, four columns per thread.
-__global__ void split_bf16_kernel(const float* x, int64_t ld, int64_t rows, int64_t cols,
-                                  __nv_bfloat16* out, int64_t ld_out, int64_t part_stride) {
-  const int64_t c4 = cols / 4;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * c4;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / c4, c = (i - r * c4) * 4;
-    const float4 v = *reinterpret_cast<const float4*>(x + r * ld + c);
-    float p[4][3];
-    split_bf16(v.x, p[0]);
-    split_bf16(v.y, p[1]);
-    split_bf16(v.z, p[2]);
-    split_bf16(v.w, p[3]);
+template <int PARTS, typename O>
+__global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
+    column_sum_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t part_stride, int64_t N,
+                      int64_t cols, O* __restrict__ out) {
+  __shared__ float sh[WARPS][SUM_COLS];
+  __shared__ float total[SUM_COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % SUM_SPLIT;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x / SUM_SPLIT) * SUM_COLS;
+  const int64_t c = c0 + lane * 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < cols) {
+    constexpr int64_t STEP = SUM_SPLIT * WARPS;
+    const int64_t step = STEP * ld;
+    int64_t r = rank * WARPS + warp;
+    const __nv_bfloat16* p = x + r * ld + c;
+    for (; r + (SUM_UNROLL - 1) * STEP < N; r += SUM_UNROLL * STEP, p += SUM_UNROLL * step) {
+      uint2 q[SUM_UNROLL][PARTS];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(p[0][k], p[1][k]),
-                             __floats2bfloat162_rn(p[2][k], p[3][k])};
-      *reinterpret_cast<uint2*>(out + k * part_stride + r * ld_out + c) =
-          *reinterpret_cast<uint2*>(h);
+      for (int u = 0; u < SUM_UNROLL; ++u)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k)
+          q[u][k] = __ldg(reinterpret_cast<const uint2*>(p + u * step + k * part_stride));
+#pragma unroll
+      for (int u = 0; u < SUM_UNROLL; ++u) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = PARTS - 1; k >= 0; --k) add4(v, q[u][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += v[i];
+      }
+    }
+    for (; r < N; r += STEP, p += step) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = PARTS - 1; k >= 0; --k)
+        add4(v, __ldg(reinterpret_cast<const uint2*>(p + k * part_stride)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sh[warp][lane * 4 + i] = s[i];
+  __syncthreads();
+  if (threadIdx.x < SUM_COLS) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += sh[w][threadIdx.x];
+    total[threadIdx.x] = v;
+  }
+  ptx::cluster_sync();
+  if (rank == 0 && threadIdx.x < SUM_COLS && c0 + threadIdx.x < cols) {
+    const uint32_t at = ptx::smem_addr(&total[threadIdx.x]);
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < SUM_SPLIT; ++r) v += ptx::ld_shared_cluster(ptx::mapa_shared(at, r));
+    out[c0 + threadIdx.x] = static_cast<O>(v);
+  }
+  ptx::cluster_sync();  // no block leaves while its sums are read
+}
+
+// ---------------------------------------------------------------------------- bf16 parts
+// Up to MAX_SPLIT_ARRAYS arrays in one launch, bound by memory (4 bytes read, 6 written per element).
+// A block takes SPLIT_VECS groups of four columns of one array; block 0 also clears the workspace
+// header, as the first launch of its call.
+constexpr int SPLIT_UNROLL = 4;
+constexpr int SPLIT_VECS = WARPS * 32 * SPLIT_UNROLL;
+
+struct SplitParams {
+  SplitArray a[MAX_SPLIT_ARRAYS];
+  int64_t first[MAX_SPLIT_ARRAYS];  // first block of each array
+  int count;
+  unsigned* header;
+};
+
+__global__ void __launch_bounds__(WARPS * 32) split_bf16_kernel(const __grid_constant__ SplitParams p) {
+  if (blockIdx.x == 0 && threadIdx.x < WS_HEADER_BYTES / 4) p.header[threadIdx.x] = 0u;
+  int k = 0;
+  while (k + 1 < p.count && p.first[k + 1] <= blockIdx.x) ++k;
+  const SplitArray& a = p.a[k];
+  const uint32_t c4 = static_cast<uint32_t>(a.cols / 4);
+  const int64_t i0 = (blockIdx.x - p.first[k]) * static_cast<int64_t>(SPLIT_VECS);
+  const int64_t r0 = i0 / c4;
+  const uint32_t o0 = static_cast<uint32_t>(i0 - r0 * c4);  // column group of the block's first
+  float4 v[SPLIT_UNROLL];
+  int64_t row[SPLIT_UNROLL];
+  uint32_t col[SPLIT_UNROLL];
+#pragma unroll
+  for (int u = 0; u < SPLIT_UNROLL; ++u) {
+    const uint32_t o = o0 + threadIdx.x + u * WARPS * 32;
+    row[u] = r0 + o / c4;
+    col[u] = o % c4 * 4;
+    if (row[u] < a.rows) v[u] = *reinterpret_cast<const float4*>(a.x + row[u] * a.ld + col[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < SPLIT_UNROLL; ++u) {
+    if (row[u] >= a.rows) break;
+    float q[4][3];
+    split_bf16(v[u].x, q[0]);
+    split_bf16(v[u].y, q[1]);
+    split_bf16(v[u].z, q[2]);
+    split_bf16(v[u].w, q[3]);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row[u] * a.ld_out + col[u];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(q[0][s], q[1][s]),
+                             __floats2bfloat162_rn(q[2][s], q[3][s])};
+      *reinterpret_cast<uint2*>(out + s * a.part_stride) = *reinterpret_cast<uint2*>(h);
     }
   }
 }
@@ -147,23 +236,34 @@ cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t str
 
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
                               int64_t part_stride, void* out, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>((cols + 127) / 128);
+  const unsigned blocks = static_cast<unsigned>((cols + SUM_COLS - 1) / SUM_COLS * SUM_SPLIT);
   const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
   if (parts == 3)
-    column_sum_kernel<__nv_bfloat16, 3><<<blocks, 128, 0, stream>>>(h, ld, part_stride, N, cols,
-                                                                    static_cast<float*>(out));
+    column_sum_kernel<3><<<blocks, WARPS * 32, 0, stream>>>(h, ld, part_stride, N, cols,
+                                                            static_cast<float*>(out));
   else
-    column_sum_kernel<__nv_bfloat16, 1>
-        <<<blocks, 128, 0, stream>>>(h, ld, 0, N, cols, static_cast<__nv_bfloat16*>(out));
+    column_sum_kernel<1><<<blocks, WARPS * 32, 0, stream>>>(h, ld, 0, N, cols,
+                                                            static_cast<__nv_bfloat16*>(out));
   return cudaGetLastError();
 }
 
-cudaError_t launch_split_bf16(const float* x, int64_t ld, int64_t rows, int64_t cols, void* out,
-                              int64_t ld_out, int64_t part_stride, cudaStream_t stream) {
-  const int64_t need = (rows * (cols / 4) + 255) / 256;
-  const unsigned blocks = static_cast<unsigned>(need < 152 * 16 ? need : 152 * 16);
-  split_bf16_kernel<<<blocks, 256, 0, stream>>>(x, ld, rows, cols, static_cast<__nv_bfloat16*>(out),
-                                                ld_out, part_stride);
+cudaError_t launch_split_bf16(const SplitArray* arrays, int count, unsigned* header,
+                              cudaStream_t stream) {
+  if (count < 1 || count > MAX_SPLIT_ARRAYS) return cudaErrorInvalidValue;
+  SplitParams p{};
+  p.count = count;
+  p.header = header;
+  int64_t blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    p.a[i] = arrays[i];
+    p.first[i] = blocks;
+    blocks += (arrays[i].rows * (arrays[i].cols / 4) + SPLIT_VECS - 1) / SPLIT_VECS;
+  }
+  if (blocks > (int64_t(1) << 31) - 1) {
+    set_error_detail("split of %lld blocks: beyond a launch's grid", static_cast<long long>(blocks));
+    return cudaErrorInvalidValue;
+  }
+  split_bf16_kernel<<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -26,6 +26,10 @@
 // steps of F32_STEP k-blocks, each into a fresh accumulator, which the epilogue warps add up in
 // registers (4e-7 there, for a drain of about 1,000 cycles per 12,000 of products).
 //
+// With few tiles (SPLIT) a cluster of 2 or 4 pairs computes each: every pair sums a piece of the K loop,
+// puts its partial sums into its ring's memory, and finishes some of the tile's boxes from all of
+// them, read through distributed shared memory in the order of the pieces.
+//
 // The outgoing gradient D and the residual R enter, and C leaves, through one 4 KB box per epilogue
 // warp (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
 // store.  Six 32 KB stages and eight boxes fill the shared memory.
@@ -36,6 +40,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <algorithm>
 
 #include "bf16_parts.cuh"
 #include "lce_act.cuh"
@@ -60,6 +66,8 @@ constexpr int CTL_BYTES = 512;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES + 1024 + CTL_BYTES;
 constexpr int RASTER = 8;               // row tiles per rasterisation group (as in lce_tc.cu)
 constexpr int MAX_JOBS = 3;
+constexpr int MAX_SPLIT = 4;             // pairs that may sum one tile: clusters of 8 CTAs
+constexpr int STATIC_WAVES = 4;         // tiles per pair up to which no scheduler counter is used
 constexpr int F32_STEP = 4;             // k-blocks per accumulator of an fp32 tile
 static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
 
@@ -91,13 +99,15 @@ struct KParams {
   int njobs, total_tiles;
   int act;
   int has_d;               // a box of R or D is loaded
+  int split;               // pairs per cluster
   const void* bias;
   int64_t m_rows;          // rows of Z
   // fp32 pre-activation gradients are written as parts, from registers
   __nv_bfloat16* parts[2];
   int64_t part_ld, part_stride;
   unsigned* err;
-  unsigned* sched;
+  unsigned* sched;         // scheduler counters, or null: tiles are dealt out round-robin
+  int clear_flags;         // the first CTA clears the error flags
 };
 
 struct FMaps {
@@ -130,23 +140,32 @@ __device__ __forceinline__ TilePos locate(const KParams& p, int t) {
   return r;
 }
 
-// A tile's K loop as steps, one accumulator each: bf16 a single step over all operand pairs, fp32
-// F32_STEP k-blocks of one pair at a time.
+// A tile's K loop as steps: single k-blocks for bf16, F32_STEP k-blocks of one operand pair (all six
+// part products) for fp32.  bf16 sums every step into one accumulator, fp32 each into its own.
 template <bool F32>
-__device__ __forceinline__ int steps_of(int nkb, int pairs) {
-  return F32 ? pairs * ((nkb + F32_STEP - 1) / F32_STEP) : 1;
+__host__ __device__ __forceinline__ int steps_per_pair(int nkb) {
+  return F32 ? (nkb + F32_STEP - 1) / F32_STEP : nkb;
+}
+
+// The steps of a tile that a CTA pair sums: all, or the part `piece` of `split` (see SPLIT below).
+struct Range {
+  int lo, hi;
+};
+__device__ __forceinline__ Range piece_of(int steps, int piece, int split) {
+  return Range{static_cast<int>(static_cast<int64_t>(steps) * piece / split),
+               static_cast<int>(static_cast<int64_t>(steps) * (piece + 1) / split)};
 }
 
 // Producer side of one tile.  A_MN, B_MN: the operand is MN-major.
 template <bool A_MN, bool B_MN, bool F32>
-__device__ __forceinline__ bool produce_tile(int nkb, int pairs, const CUtensorMap* mA,
+__device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, const CUtensorMap* mA,
                                              const CUtensorMap* mB, int m0, int n0, uint32_t base,
                                              Ctl* ctl, Ring& r, volatile int* abort_flag,
-                                             unsigned* err, uint32_t rank) {
+                                             unsigned* err, uint32_t rank, uint32_t leader) {
   auto block = [&](const CUtensorMap* a, const CUtensorMap* b, int k0, int za, int zb) {
     const uint32_t full_local = ptx::smem_addr(&ctl->full[r.stage]);
     if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, err)) return false;
-    const uint32_t full = ptx::mapa_shared(full_local, 0);
+    const uint32_t full = ptx::mapa_shared(full_local, leader);
     if (rank == 0) ptx::mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
     const uint32_t sa = base + r.stage * STAGE_BYTES, sb = sa + A_BYTES;
     if (A_MN) {
@@ -166,17 +185,20 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, const CUtensorM
     if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
     return true;
   };
+  const int per_pair = steps_per_pair<F32>(nkb);
   for (int pr = 0; pr < pairs; ++pr) {
     const CUtensorMap* a = &mA[pr];
     const CUtensorMap* b = &mB[pr];
-    if (!F32) {
-      for (int kb = 0; kb < nkb; ++kb)
-        if (!block(a, b, kb * BK, 0, 0)) return false;
-    } else {
-      for (int kb0 = 0; kb0 < nkb; kb0 += F32_STEP)
+    const int lo = max(range.lo - pr * per_pair, 0), hi = min(range.hi - pr * per_pair, per_pair);
+    for (int st = lo; st < hi; ++st) {
+      if (!F32) {
+        if (!block(a, b, st * BK, 0, 0)) return false;
+      } else {
+        const int end = min(nkb, (st + 1) * F32_STEP);
         for (int s = 0; s < 6; ++s)
-          for (int kb = kb0; kb < min(nkb, kb0 + F32_STEP); ++kb)
+          for (int kb = st * F32_STEP; kb < end; ++kb)
             if (!block(a, b, kb * BK, part_a(s), part_b(s))) return false;
+      }
     }
   }
   return true;
@@ -184,7 +206,7 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, const CUtensorM
 
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t base, Ctl* ctl, Ring& r,
-                                         volatile int* abort_flag, unsigned* err) {
+                                         volatile int* abort_flag, unsigned* err, uint16_t pair_mask) {
   constexpr uint32_t IDESC = ptx::idesc_bf16_f32(TILE, TILE, A_MN, B_MN);
   for (int kb = 0; kb < blocks; ++kb) {
     if (!wait_bar(ptx::smem_addr(&ctl->full[r.stage]), r.ph, abort_flag, err)) return false;
@@ -194,7 +216,7 @@ __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t b
     for (int k = 0; k < BK / 16; ++k)
       ptx::tc_mma_f16_pair(d_tmem, A_MN ? desc_mnmajor(sa, k) : desc_kmajor(sa, k),
                            B_MN ? desc_mnmajor(sb, k) : desc_kmajor(sb, k), IDESC, (kb | k) != 0);
-    ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[r.stage]), 0x3);
+    ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[r.stage]), pair_mask);
     if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
   }
   return true;
@@ -312,7 +334,7 @@ __device__ __forceinline__ void store_parts(const float (&v)[32], __nv_bfloat16*
   }
 }
 
-template <int MODE, bool F32>
+template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     ffn_tc_kernel(const __grid_constant__ FMaps maps, const KParams p) {
   constexpr bool GATED = kGated<MODE>;
@@ -327,10 +349,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();  // 0 = the pair's MMA issuer
-  const int units = static_cast<int>(gridDim.x >> 1);
+  // A cluster is one pair, or with SPLIT several, each summing a piece of the same tile's K loop.
+  const uint32_t crank = ptx::cluster_ctarank();
+  const uint32_t rank = SPLIT ? crank & 1u : crank;  // 0 = the pair's MMA issuer
+  const uint32_t leader = SPLIT ? crank & ~1u : 0u;  // cluster rank of the issuer
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
+  const int split = SPLIT ? p.split : 1, piece = static_cast<int>(leader >> 1);
+  const int units = static_cast<int>(gridDim.x >> 1) / split;
+  const int unit = static_cast<int>(blockIdx.x >> 1) / split;
 
   if (threadIdx.x == 0) {
+    // the first CTA is among the first to run, and a wait gives up only WAIT_LIMIT_NS after that
+    if (p.clear_flags && blockIdx.x == 0) *p.err = 0u;
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
@@ -358,18 +388,111 @@ __global__ void __launch_bounds__(THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
 
+  // Epilogue warps: the warp's box, and the work on one box of results.
+  const int e = (warp + 6) & 7;  // warps 2..9
+  const int q = warp & 3;        // TMEM lane quadrant the warp may access
+  const int half = e >> 2;       // which half of the columns it drains
+  constexpr int UC = F32 ? 32 : 64;          // columns of one box
+  constexpr int COLS = GATED ? HALF : TILE;  // output columns of a tile
+  constexpr int UNITS = COLS / 2 / UC;       // boxes per warp and tile
+  const uint32_t box = boxes + e * STAGE_BUF_BYTES;
+  const uint32_t box_bar = ptx::smem_addr(&ctl->box[e]);
+  const uint32_t row_addr = box + lane * 128, sw = lane & 7;
+  const bool has_d = DZ || (MODE == FFN_LINEAR && p.has_d);
+  uint32_t box_ph = 0;
+  bool in_flight = false;
+  int split_tile = -1;
+  // R or D into the box, once the store before it has been read
+  auto fetch = [&](int col, int box_row) {
+    if (lane == 0) {
+      ptx::bulk_wait_read<0>();
+      ptx::mbar_arrive_expect_tx(box_bar, STAGE_BUF_BYTES);
+      ptx::tma_load_2d(box, &maps.d, col, box_row, box_bar);
+    }
+    in_flight = true;
+  };
+  // One box of results: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32 accumulator
+  // columns of the thread's row.  False when a wait gave up.
+  auto process = [&](const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load) {
+    if (has_d) {
+      if (!wait_bar(box_bar, box_ph, abort_flag, p.err)) return false;
+      in_flight = false;
+      box_ph ^= 1u;
+    } else {
+      if (lane == 0) ptx::bulk_wait_read<0>();
+      __syncwarp();
+    }
+    [[maybe_unused]] uint32_t keep[MODE == FFN_GATED_DGU && !F32 ? 32 : 1];
+#pragma unroll
+    for (int h = 0; h < UC / 32; ++h) {
+      float z[32], u[32];
+      load(h, z, u);
+      if constexpr (MODE == FFN_GRADS)
+        epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols, nullptr,
+                                            false);
+      else
+        dispatch_act(p.act, [&](auto tag) {
+          epilogue32<MODE, decltype(tag)::value, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols,
+                                                      p.bias, has_d);
+        });
+      if constexpr (MODE == FFN_GATED_DGU && !F32) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) keep[h * 16 + i] = pack2(z[2 * i], z[2 * i + 1]);
+      }
+      if constexpr (DZ && F32) {
+        const int64_t row = box_row + lane;
+        if (row < p.m_rows) {
+          const int64_t off = row * p.part_ld + col;
+          store_parts(z, p.parts[0] + off, p.part_stride, c_cols - col);
+          if (GATED) store_parts(u, p.parts[1] + off, p.part_stride, c_cols - col);
+        }
+      }
+    }
+    if constexpr (!(DZ && F32)) {
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_2d(mC, box, col, box_row);
+        ptx::bulk_commit();
+      }
+      if constexpr (MODE == FFN_GATED_DGU) {
+        if (lane == 0) ptx::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          ptx::st_shared_v4(row_addr + ((static_cast<uint32_t>(c) ^ sw) << 4), keep[4 * c],
+                            keep[4 * c + 1], keep[4 * c + 2], keep[4 * c + 3]);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&maps.c2, box, col, box_row);
+          ptx::bulk_commit();
+        }
+      }
+    } else {
+      // every lane has read its row before the next box may land on it
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+    }
+    return true;
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
       bool ok = true;
       Ring ring{0, 0u};
-      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0};
-      unsigned next = 0u;
+      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0, leader};
+      unsigned next = unit;
       int upcoming = -1;
+      auto draw = [&] {  // the ticket after `next`
+        if (p.sched) next = atomicAdd(&p.sched[0], 1u);
+        else next += units;
+      };
       if (rank == 0) {
-        next = atomicAdd(&p.sched[0], 1u);
+        if (p.sched) draw();
         upcoming = tq.post(next, p.sched, p.total_tiles, units);
-        if (upcoming >= 0) next = atomicAdd(&p.sched[0], 1u);
+        if (upcoming >= 0) draw();
       }
       while (ok) {
         int tile;
@@ -377,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tile = upcoming;
           if (tile < 0) break;
           upcoming = tq.post(next, p.sched, p.total_tiles, units);
-          if (upcoming >= 0) next = atomicAdd(&p.sched[0], 1u);
+          if (upcoming >= 0) draw();
         } else {
           tile = tq.take(1u);
         }
@@ -385,23 +508,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         const TilePos tp = locate(p, tile);
         const Job& jb = p.job[tp.job];
         const int m0 = tp.tm * TILE + static_cast<int>(rank) * BM;
+        const Range range = piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, piece, split);
         if constexpr (GATED) {
           // CTA 0 loads its columns' rows of Wg, CTA 1 the same rows of Wu
-          ok = produce_tile<false, false, F32>(jb.nkb, 1, maps.a[0], &maps.b[0][rank], m0,
+          ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
                                                tp.tn * HALF, base, ctl, ring, abort_flag, p.err,
-                                               rank);
+                                               rank, leader);
         } else {
           const int n0 = tp.tn * TILE + static_cast<int>(rank) * HALF;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = produce_tile<true, true, F32>(jb.nkb, jb.pairs, maps.a[tp.job], maps.b[tp.job], m0,
-                                                 n0, base, ctl, ring, abort_flag, p.err, rank);
+              ok = produce_tile<true, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+                                                 maps.b[tp.job], m0, n0, base, ctl, ring, abort_flag,
+                                                 p.err, rank, leader);
             else
-              ok = produce_tile<false, true, F32>(jb.nkb, jb.pairs, maps.a[tp.job], maps.b[tp.job],
-                                                  m0, n0, base, ctl, ring, abort_flag, p.err, rank);
+              ok = produce_tile<false, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+                                                  maps.b[tp.job], m0, n0, base, ctl, ring,
+                                                  abort_flag, p.err, rank, leader);
           } else {
-            ok = produce_tile<false, false, F32>(jb.nkb, 1, maps.a[0], maps.b[0], m0, n0, base, ctl,
-                                                 ring, abort_flag, p.err, rank);
+            ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
+                                                 ctl, ring, abort_flag, p.err, rank, leader);
           }
         }
       }
@@ -418,16 +544,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       Ring ring{0, 0u};
       int acc = 0;
       uint32_t aph = 0;
-      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, false};
+      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, false, leader};
       while (ok) {
         const int tile = tq.take(1u);
         if (tile < 0) break;
         const TilePos tp = locate(p, tile);
         const Job& jb = p.job[tp.job];
-        const int steps = steps_of<F32>(jb.nkb, jb.pairs), per_pair = steps / jb.pairs;
-        for (int st = 0; ok && st < steps; ++st) {
-          const int blocks =
-              F32 ? 6 * min(F32_STEP, jb.nkb - (st % per_pair) * F32_STEP) : jb.nkb * jb.pairs;
+        const int per_pair = steps_per_pair<F32>(jb.nkb);
+        const Range range = piece_of(per_pair * jb.pairs, piece, split);
+        for (int st = range.lo; ok && (st < range.hi || st == range.lo); ++st) {
+          // an empty piece still hands its accumulator over; no one reads it
+          const int blocks = range.hi == range.lo ? 0
+                             : F32 ? 6 * min(F32_STEP, jb.nkb - (st % per_pair) * F32_STEP)
+                                   : range.hi - range.lo;
           if (!wait_bar(ptx::smem_addr(&ctl->tempty[acc]), aph ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
@@ -435,167 +564,147 @@ __global__ void __launch_bounds__(THREADS, 1)
           ptx::tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * TILE;
           if constexpr (MODE == FFN_GRADS) {
-            if (jb.mn) ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
-            else ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
+            if (jb.mn)
+              ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+            else
+              ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
           } else {
-            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err);
+            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
           }
           if (!ok) break;
-          ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), 0x3);
+          ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), pair_mask);
           acc ^= 1;
           if (acc == 0) aph ^= 1u;
+          if (!F32) break;  // one accumulator for the whole range
         }
       }
       if (!ok) {
         // Make sure no MMA is still writing TMEM before it is released.
-        ptx::tc_commit_pair(ptx::smem_addr(&ctl->drain), 0x1);
+        ptx::tc_commit_pair(ptx::smem_addr(&ctl->drain), static_cast<uint16_t>(1u << leader));
         wait_bar_drain(ptx::smem_addr(&ctl->drain), 0, 100000000ull);
       }
     }
   } else {
     // ------------------------------------------------------------------ epilogue (warps 2..9)
-    const int e = warp - 2;
-    const int q = warp & 3;       // TMEM lane quadrant this warp may access
-    const int half = e >> 2;      // which half of the columns
-    constexpr int UC = F32 ? 32 : 64;          // columns of one box
-    constexpr int COLS = GATED ? HALF : TILE;  // output columns of a tile
-    constexpr int UNITS = COLS / 2 / UC;       // boxes per warp and tile
-    const uint32_t box = boxes + e * STAGE_BUF_BYTES;
-    const uint32_t box_bar = ptx::smem_addr(&ctl->box[e]);
-    const uint32_t row_addr = box + lane * 128, sw = lane & 7;
-    const bool has_d = DZ || (MODE == FFN_LINEAR && p.has_d);
-    uint32_t box_ph = 0;
+    TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0, leader};
     int acc = 0;
     uint32_t aph = 0;
-    bool ok = true, in_flight = false;
-    TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0};
+    bool ok = true;
     while (ok) {
       const int tile = tq.take(0xffffffffu);
       if (tile < 0) break;
       const TilePos tp = locate(p, tile);
       const Job& jb = p.job[tp.job];
-      const CUtensorMap* mC = &maps.c[tp.job];
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      const Range range = piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, piece, split);
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
       const int col0 = tp.tn * COLS + half * (COLS / 2);
-      // R or D of a unit into the box, once the store before it has been read
-      auto fetch = [&](int col) {
-        if (lane == 0) {
-          ptx::bulk_wait_read<0>();
-          ptx::mbar_arrive_expect_tx(box_bar, STAGE_BUF_BYTES);
-          ptx::tma_load_2d(box, &maps.d, col, box_row, box_bar);
-        }
-        in_flight = true;
-      };
-      if (has_d && col0 < jb.c_cols) fetch(col0);
+      // R or D of the first box, while the products run
+      if (!SPLIT && has_d && col0 < jb.c_cols) fetch(col0, box_row);
       // hand the accumulator back to the MMA issuer (in the pair's first CTA)
       auto release = [&]() {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0)
-          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tempty[acc]), 0));
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tempty[acc]), leader));
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
       };
-      if (F32) {
+      const int steps = F32 ? max(range.hi - range.lo, 1) : 1;
+      if (F32 && steps > 1) {
         // sum the steps' accumulators; the total goes back into the last one's columns
-        const int steps = steps_of<F32>(jb.nkb, jb.pairs);
-        if (steps > 1) {
-          float sum[4][32];
+        float sum[4][32];
 #pragma unroll
-          for (int i = 0; i < 128; ++i) sum[i >> 5][i & 31] = 0.f;
+        for (int i = 0; i < 128; ++i) sum[i >> 5][i & 31] = 0.f;
 #pragma unroll 1
-          for (int st = 0; st < steps; ++st) {
-            if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) { ok = false; break; }
-            ptx::tc_fence_after();
+        for (int st = 0; st < steps; ++st) {
+          if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) { ok = false; break; }
+          ptx::tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-              ptx::tmem_add16(lanes + acc * TILE + half_col<GATED>(half, h >> 1) + (h & 1) * 16,
-                              &sum[h >> 1][(h & 1) * 16]);
-            if (st + 1 < steps) release();
-          }
-          if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            ptx::tmem_store32(lanes + acc * TILE + half_col<GATED>(half, h), sum[h]);
+          for (int h = 0; h < 8; ++h)
+            ptx::tmem_add16(lanes + acc * TILE + half_col<GATED>(half, h >> 1) + (h & 1) * 16,
+                            &sum[h >> 1][(h & 1) * 16]);
+          if (st + 1 < steps) release();
         }
-      }
-      if (!(F32 && steps_of<F32>(jb.nkb, jb.pairs) > 1) &&
-          !wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err))
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          ptx::tmem_store32(lanes + acc * TILE + half_col<GATED>(half, h), sum[h]);
+      } else if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) {
         break;
+      }
       ptx::tc_fence_after();
       const uint32_t tbase = lanes + acc * TILE;
+      if constexpr (SPLIT) {
+        // This pair's partial sums into shared memory, [column][row]: every MMA is done, so the ring
+        // is free.  A cluster computes one tile: the boxes follow below, once all pairs are here.
 #pragma unroll 1
-      for (int un = 0; un < UNITS; ++un) {
-        const int col = col0 + un * UC;
-        if (col >= jb.c_cols) break;  // same for every thread of the warp
-        if (has_d) {
-          if (un > 0) fetch(col);
-          if (!wait_bar(box_bar, box_ph, abort_flag, p.err)) { ok = false; break; }
-          in_flight = false;
-          box_ph ^= 1u;
-        } else {
-          if (lane == 0) ptx::bulk_wait_read<0>();
-          __syncwarp();
-        }
-        uint32_t keep[MODE == FFN_GATED_DGU && !F32 ? 32 : 1];
+        for (int h = 0; h < 4; ++h) {
+          const int c = half_col<GATED>(half, h);
+          float v[32];
+          ptx::tmem_load32(tbase + c, v);
 #pragma unroll
-        for (int h = 0; h < UC / 32; ++h) {
-          const int at = half * (COLS / 2) + un * UC + h * 32;  // accumulator column
-          float z[32], u[32];
-          ptx::tmem_load32(tbase + at, z);
-          if (GATED) ptx::tmem_load32(tbase + HALF + at, u);
-          if constexpr (MODE == FFN_GRADS)
-            epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, jb.c_cols,
-                                                nullptr, false);
-          else
-            dispatch_act(p.act, [&](auto tag) {
-              epilogue32<MODE, decltype(tag)::value, F32>(z, u, row_addr, sw, h * 4, col + h * 32,
-                                                          jb.c_cols, p.bias, has_d);
-            });
-          if constexpr (MODE == FFN_GATED_DGU && !F32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) keep[h * 16 + i] = pack2(z[2 * i], z[2 * i + 1]);
-          }
-          if constexpr (DZ && F32) {
-            const int64_t row = box_row + lane;
-            if (row < p.m_rows) {
-              const int64_t off = row * p.part_ld + col;
-              store_parts(z, p.parts[0] + off, p.part_stride, jb.c_cols - col);
-              if (GATED) store_parts(u, p.parts[1] + off, p.part_stride, jb.c_cols - col);
-            }
-          }
+          for (int i = 0; i < 32; ++i)
+            ptx::st_shared_f32(base + ((c + i) * BM + q * 32 + lane) * 4, v[i]);
         }
-        if constexpr (!(DZ && F32)) {
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            ptx::tma_store_2d(mC, box, col, box_row);
-            ptx::bulk_commit();
-          }
-          if constexpr (MODE == FFN_GATED_DGU) {
-            if (lane == 0) ptx::bulk_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              ptx::st_shared_v4(row_addr + ((static_cast<uint32_t>(c) ^ sw) << 4), keep[4 * c],
-                                keep[4 * c + 1], keep[4 * c + 2], keep[4 * c + 3]);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::tma_store_2d(&maps.c2, box, col, box_row);
-              ptx::bulk_commit();
-            }
-          }
-        } else {
-          // every lane has read its row before the next box may land on it
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
+        release();
+        split_tile = tile;
+      } else {
+#pragma unroll 1
+        for (int un = 0; un < UNITS; ++un) {
+          const int col = col0 + un * UC;
+          if (col >= jb.c_cols) break;  // same for every thread of the warp
+          if (has_d && un > 0) fetch(col, box_row);
+          const int at = half * (COLS / 2) + un * UC;  // accumulator column
+          ok = process(&maps.c[tp.job], jb.c_cols, col, box_row, [&](int h, float (&z)[32], float (&u)[32]) {
+            ptx::tmem_load32(tbase + at + h * 32, z);
+            if (GATED) ptx::tmem_load32(tbase + HALF + at + h * 32, u);
+          });
+          if (!ok) break;
         }
+        if (!ok) break;
+        release();
       }
-      if (!ok) break;
-      release();
     }
+  }
+
+  if constexpr (SPLIT) {
+    __syncwarp();
+    ptx::cluster_sync();  // every pair's partial sums are written
+    if (warp >= 2 && split_tile >= 0) {
+      const TilePos tp = locate(p, split_tile);
+      const Job& jb = p.job[tp.job];
+      const int steps = steps_per_pair<F32>(jb.nkb) * jb.pairs;
+      const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
+      // box b is finished by pair b % split, its warps of column half (b / split) % 2
+#pragma unroll 1
+      for (int b = piece; b < COLS / UC; b += split) {
+        if (((b / split) & 1) != half) continue;
+        const int col = tp.tn * COLS + b * UC;
+        if (col >= jb.c_cols) break;
+        if (has_d) fetch(col, box_row);
+        const bool ok = process(&maps.c[tp.job], jb.c_cols, col, box_row, [&](int h, float (&z)[32], float (&u)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[i] = u[i] = 0.f;
+          const uint32_t at = base + ((b * UC + h * 32) * BM + q * 32 + lane) * 4;
+#pragma unroll 1
+          for (int s = 0; s < split; ++s) {  // in the order of the pieces
+            const Range r = piece_of(steps, s, split);
+            if (r.lo == r.hi) continue;
+            const uint32_t peer = ptx::mapa_shared(at, 2 * s + rank);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] += ptx::ld_shared_cluster(peer + i * BM * 4);
+            if (GATED) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] += ptx::ld_shared_cluster(peer + (HALF + i) * BM * 4);
+            }
+          }
+        });
+        if (!ok) break;
+      }
+    }
+  }
+  if (warp >= 2) {
     if (in_flight) wait_bar_drain(box_bar, box_ph, 100000000ull);
     if (lane == 0) ptx::bulk_wait<0>();  // this warp's output stores have landed
     __syncwarp();
@@ -649,41 +758,84 @@ bool operand(CUtensorMap* m, const FfnOperand& o, bool mn, const char* what) {
                   ps, what);
 }
 
+// What decides how a launch's sums are cut: all its products, asked for or not, so that a result is
+// the same bits whichever others are computed with it.
+struct Plan {
+  int tiles, longest;  // tiles, and steps of the longest K loop
+};
+
+// Largest grid, in clusters of `pairs` CTA pairs, that the device holds at once (0: unknown).
 template <int MODE, bool F32>
-cudaError_t launch(const FMaps& maps, const KParams& p, int num_sms, cudaStream_t stream) {
+int max_clusters(int pairs) {
+  static int cached[MAX_SPLIT + 1];
+  if (cached[pairs] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * pairs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, ffn_tc_kernel<MODE, F32, true>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
+    }
+    cached[pairs] = n > 0 ? n : -1;
+  }
+  return cached[pairs] > 0 ? cached[pairs] : 0;
+}
+
+template <int MODE, bool F32>
+cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, int num_sms,
+                   cudaStream_t stream) {
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32>,
+    cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) {
       set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(e));
       return e;
     }
     attr_set = true;
   }
+  // Few tiles: each is summed by 2 or 4 pairs, as long as all clusters run at once and the longest
+  // K loop leaves every pair at least 8 k-blocks.
+  p.split = 1;
+  for (int k = 2; k <= MAX_SPLIT; k *= 2)
+    if (plan.longest >= (F32 ? 2 : 8) * k && plan.tiles <= max_clusters<MODE, F32>(k)) p.split = k;
   const int units = num_sms / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (p.total_tiles < units ? p.total_tiles : units), 1, 1);
+  cfg.gridDim = dim3(2 * (p.split > 1 ? p.total_tiles * p.split : std::min(p.total_tiles, units)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * p.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32>, maps, p);
+  cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, true>, maps, p)
+                              : cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, false>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
-    set_error_detail("launch of a feed-forward product (mode %d, %d tiles): %s", MODE, p.total_tiles,
-                     cudaGetErrorName(e));
+    set_error_detail("launch of a feed-forward product (mode %d, %d tiles, split %d): %s", MODE,
+                     p.total_tiles, p.split, cudaGetErrorName(e));
   return e;
 }
 
 template <bool F32>
-cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, int num_sms, cudaStream_t stream) {
+cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, HeaderState* state, int num_sms,
+                cudaStream_t stream) {
   FMaps maps;
   memset(&maps, 0, sizeof(maps));
   KParams p{};
@@ -691,13 +843,15 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, int num_sms, cud
   const bool gated = mode == FFN_GATED || mode == FFN_GATED_DGU;
   const bool dz = mode == FFN_LINEAR_DZ || mode == FFN_GATED_DGU;
   const uint32_t uc = F32 ? 32 : 64;
-  for (int j = 0; j < njobs; ++j) {
-    const FfnTc& g = jobs[j];
-    Job& jb = p.job[j];
+  Plan plan{0, 0};
+  int n = 0;
+  for (int i = 0; i < njobs; ++i) {
+    const FfnTc& g = jobs[i];
+    Job jb{};
     const int64_t cols = gated ? HALF : TILE;
     const int64_t tm = (g.M + TILE - 1) / TILE, tn = (g.Ncols + cols - 1) / cols;
     const int64_t nkb = (g.K + BK - 1) / BK;
-    if (tm * tn > (int64_t(1) << 28) || p.total_tiles + tm * tn > (int64_t(1) << 29) || nkb > (1 << 25)) {
+    if (tm * tn > (int64_t(1) << 28) || plan.tiles + tm * tn > (int64_t(1) << 29) || nkb > (1 << 25)) {
       set_error_detail("feed-forward product of %lld x %lld tiles: beyond the scheduler's range",
                        static_cast<long long>(tm), static_cast<long long>(tn));
       return cudaErrorInvalidValue;
@@ -709,6 +863,11 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, int num_sms, cud
     jb.pairs = (!gated && g.A2.ptr) ? 2 : 1;
     jb.mn = g.a_mn;
     jb.c_cols = static_cast<int>(g.Ncols);
+    plan.tiles += jb.num_tiles;
+    plan.longest = std::max(plan.longest, steps_per_pair<F32>(jb.nkb) * jb.pairs);
+    if (!g.C) continue;  // a result that is not asked for counts in the plan only
+    const int j = n++;
+    p.job[j] = jb;
     p.total_tiles += jb.num_tiles;
     if (!operand(&maps.a[j][0], g.A, g.a_mn, "A") || !operand(&maps.b[j][0], g.B, g.b_mn, "B"))
       return cudaErrorInvalidResourceHandle;
@@ -724,8 +883,9 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, int num_sms, cud
         return cudaErrorInvalidResourceHandle;
     }
   }
+  if (n == 0) return cudaSuccess;
   const FfnTc& g = jobs[0];
-  p.njobs = njobs;
+  p.njobs = n;
   p.act = g.act;
   p.bias = g.bias;
   p.m_rows = g.M;
@@ -740,23 +900,37 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, int num_sms, cud
     p.part_stride = g.part_stride;
   }
   p.err = header;
-  p.sched = header + WS_SCHED_WORD;
+  // A few waves of tiles are dealt out round-robin, which needs nothing cleared beforehand; longer
+  // launches take tickets from the counters in the header, which keeps tiles that share operands
+  // together however unevenly the SMs progress.
+  if (p.total_tiles > STATIC_WAVES * (num_sms / 2)) {
+    p.sched = header + WS_SCHED_WORD;
+    const size_t from = state->flags ? WS_SCHED_WORD * sizeof(unsigned) : 0;
+    if (!state->sched) {
+      cudaError_t e = cudaMemsetAsync(reinterpret_cast<char*>(header) + from, 0, WS_HEADER_BYTES - from,
+                                      stream);
+      if (e != cudaSuccess) return e;
+      state->flags = state->sched = true;  // the launch leaves the counters at zero
+    }
+  }
+  p.clear_flags = !state->flags;
+  state->flags = true;
   switch (mode) {
-    case FFN_LINEAR: return launch<FFN_LINEAR, F32>(maps, p, num_sms, stream);
-    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, num_sms, stream);
-    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, num_sms, stream);
-    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, num_sms, stream);
-    default: return launch<FFN_GRADS, F32>(maps, p, num_sms, stream);
+    case FFN_LINEAR: return launch<FFN_LINEAR, F32>(maps, p, plan, num_sms, stream);
+    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, plan, num_sms, stream);
+    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, plan, num_sms, stream);
+    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, plan, num_sms, stream);
+    default: return launch<FFN_GRADS, F32>(maps, p, plan, num_sms, stream);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
-                          int num_sms, cudaStream_t stream) {
+                          HeaderState* state, int num_sms, cudaStream_t stream) {
   if (njobs < 1 || njobs > MAX_JOBS) return cudaErrorInvalidValue;
-  return dtype == LCE_BF16 ? run<false>(jobs, njobs, header, num_sms, stream)
-                           : run<true>(jobs, njobs, header, num_sms, stream);
+  return dtype == LCE_BF16 ? run<false>(jobs, njobs, header, state, num_sms, stream)
+                           : run<true>(jobs, njobs, header, state, num_sms, stream);
 }
 
 }  // namespace lce

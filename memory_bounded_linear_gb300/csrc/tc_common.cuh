@@ -94,6 +94,7 @@ struct TileQueue {
   // which does not make them wait the way the cluster-scope one does (measured: the MMA thread
   // spent 5-14% of its time in a cluster-scope hand-back)
   bool remote;
+  uint32_t leader = 0;  // cluster rank of the pair's first CTA
 
   __device__ __forceinline__ void advance() {
     if (++slot == TQ) { slot = 0; ph ^= 1u; }
@@ -101,7 +102,8 @@ struct TileQueue {
 
   // Scheduler: posts `ticket` (taken from the counter sched[0] beforehand) to both CTAs, or -1
   // when it is past the last tile.  Returns what was posted (-1 also after a timeout); the last
-  // unit to receive -1 clears the counters for the next launch.
+  // unit to receive -1 clears the counters for the next launch.  sched may be null: the caller
+  // draws its tickets without counters.
   __device__ __forceinline__ int post(unsigned ticket, unsigned* sched, int num_tiles, int units) {
     const uint32_t empty = ptx::smem_addr(&ctl->tq_empty[slot]);
     if (!wait_bar<PAIR>(empty, ph ^ 1u, abort_flag, err)) return -1;
@@ -109,12 +111,12 @@ struct TileQueue {
     ctl->tq[slot] = t;
     const uint32_t full = ptx::smem_addr(&ctl->tq_full[slot]);
     if (PAIR) {
-      ptx::st_shared_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tq[slot]), 1), t);
-      ptx::mbar_arrive_cluster(ptx::mapa_shared(full, 1));
+      ptx::st_shared_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tq[slot]), leader + 1), t);
+      ptx::mbar_arrive_cluster(ptx::mapa_shared(full, leader + 1));
     }
     ptx::mbar_arrive(full);
     advance();
-    if (t < 0 && atomicAdd(&sched[1], 1u) == static_cast<unsigned>(units - 1)) {
+    if (t < 0 && sched && atomicAdd(&sched[1], 1u) == static_cast<unsigned>(units - 1)) {
       atomicExch(&sched[0], 0u);
       atomicExch(&sched[1], 0u);
     }
@@ -130,7 +132,7 @@ struct TileQueue {
     __syncwarp(mask);
     if ((threadIdx.x & 31) == static_cast<unsigned>(__ffs(mask) - 1)) {
       const uint32_t empty = ptx::smem_addr(&ctl->tq_empty[slot]);
-      if (remote) ptx::mbar_arrive_cluster(ptx::mapa_shared(empty, 0));
+      if (remote) ptx::mbar_arrive_cluster(ptx::mapa_shared(empty, leader));
       else ptx::mbar_arrive(empty);
     }
     advance();

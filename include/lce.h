@@ -402,7 +402,7 @@ int32_t lce_trace_end(void);
  * the exact fp32 path: "simt_fwd_lse", "simt_bwd_grad", "simt_dh", "simt_dw"; and "combine",
  * "finalize", "split_tf32".  Feed-forward operators: "linear", "linear_dz", "gated",
  * "gated_dg_du" (the gradients of the pre-activations), "ffn_grads" (dX and / or the weight
- * gradients), "column_sum" (dbias), "split_bf16" (fp32 operands into bf16 parts).  Clipping:
+ * gradients), "column_sum" (dbias), "pack" (copies of operands).  Clipping:
  * "grad_norm", "grad_scale".
  */
 const char* lce_kernel_name(int32_t kernel_id);

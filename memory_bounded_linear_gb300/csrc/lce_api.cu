@@ -686,7 +686,7 @@ const char* lce_kernel_name(int32_t id) {
                                      "tc_bwd_grad",   "tc_dh_dw", "linear",
                                      "linear_dz",     "gated",    "gated_dg_du",
                                      "ffn_grads",     "column_sum", "grad_norm",
-                                     "grad_scale",    "split_bf16"};
+                                     "grad_scale",    "pack"};
   return (id >= 0 && id < K_NUM) ? names[id] : nullptr;
 }
 

@@ -57,35 +57,39 @@ struct FfnTc {
   int64_t part_stride;
 };
 
-// What is known to be zero in the workspace header when a launch is made; a launch updates it.
-struct HeaderState {
+// State of a call between its launches (each updates it): what is known to be zero in the workspace
+// header.
+struct CallState {
   bool flags = false;  // the error flags
   bool sched = false;  // the scheduler counters
+  bool dependent = false;  // the stream's last kernel is this call's: the next may be a dependent launch
 };
 
 // Tensor cores: lce_ffn_tc.cu.  Several jobs only for FFN_GRADS, where a job whose C is null is not
 // computed but counted when the launch is planned; header: the workspace header.
 cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
-                          HeaderState* state, int num_sms, cudaStream_t stream);
-// fp32 x [rows x cols], row stride ld, into three bf16 parts of row stride ld_out, part_stride
-// apart, for several arrays; clears the workspace header: lce_ffn_simt.cu
-struct SplitArray {
-  const float* x;
+                          CallState* state, int num_sms, cudaStream_t stream);
+// Copies of x [rows x cols], row stride ld, for several arrays: fp32 into three bf16 parts (parts = 3)
+// of row stride ld_out, part_stride apart, or bf16 into rows of stride ld_out (parts = 1).  Clears the
+// workspace header: lce_ffn_simt.cu
+struct PackArray {
+  const void* x;
   int64_t ld, rows, cols;
   void* out;
   int64_t ld_out, part_stride;
 };
-constexpr int MAX_SPLIT_ARRAYS = 3;
-cudaError_t launch_split_bf16(const SplitArray* arrays, int count, unsigned* header,
-                              cudaStream_t stream);
+constexpr int MAX_PACK_ARRAYS = 3;
+cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned* header,
+                        cudaStream_t stream);
 // Few tokens, bf16 (at most FFN_FEW_TOKENS rows): lce_ffn_few.cu.  Clears the error flags.
 constexpr int64_t FFN_FEW_TOKENS = 128;
 cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream);
 // Few tokens, fp32: lce_ffn_simt.cu.  Clears the error flags.
 cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream);
 // out[c] = sum over the N rows of x[., c], row stride ld.  parts = 1: x and out bf16; parts = 3: x
-// holds three bf16 parts, part_stride apart, and out is fp32: lce_ffn_simt.cu
+// holds three bf16 parts, part_stride apart, and out is fp32; dependent: the stream's last kernel is
+// this call's: lce_ffn_simt.cu
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
-                              int64_t part_stride, void* out, cudaStream_t stream);
+                              int64_t part_stride, void* out, bool dependent, cudaStream_t stream);
 
 }  // namespace lce

@@ -31,18 +31,30 @@ bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
 // lce_ffn_simt.cu), larger ones on the kernel whose tiles hold 256 tokens.
 bool few_tokens(int64_t N, lce_dtype_t dt) { return N <= (dt == LCE_BF16 ? FFN_FEW_TOKENS : 32); }
 
-int64_t round8(int64_t x) { return (x + 7) & ~int64_t(7); }
+// Rows of the workspace's arrays start on 128-byte lines.
+int64_t round64(int64_t x) { return (x + 63) & ~int64_t(63); }
 
-// One array of the workspace.  LCE_BF16: [rows x cols] bf16.  LCE_F32: three bf16 parts of it, rows
-// padded to 16 bytes.
+// Whether a bf16 operand with rows of `width` elements is copied into aligned rows before the products
+// read it.  Rows that start between 32-byte sectors cost the tensor-core kernel a third of its rate
+// (10240 x 1672 x 3008: 96 us, 1664 wide 68 us); the copy costs a pass over the operand, which pays
+// when every element enters enough products.  Rows whose stride is a multiple of 32 bytes but not
+// of 128 lose 10% and are left alone.
+bool misaligned(int64_t width) { return width % 16 != 0; }
+bool copy_pays(int64_t N, int64_t width, bool backward) {
+  return N * width >= (backward ? 600 : 1200) * (N + width);
+}
+
+// One array of the workspace: bf16, or for LCE_F32 three bf16 parts of it.
 struct Slot {
   size_t off;
   int64_t ld, part_stride;
 };
 
-// Workspace: header (error flags, scheduler counters), then for LCE_F32 the parts of X and of the
-// weights (products on the tensor cores), then the gradients of the pre-activations.
+// Workspace: header (error flags, scheduler counters), then the copies of X and of the weights that
+// the tensor-core kernel reads (LCE_F32: their parts; LCE_BF16: where copy_pays), then the gradients
+// of the pre-activations.
 struct Layout {
+  bool copies;
   Slot x, w[2], z[2];
   size_t total;
 };
@@ -53,11 +65,13 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
   size_t off = WS_HEADER_BYTES;
   auto take = [&](Slot& s, int64_t rows, int64_t cols) {
     s.off = off;
-    s.ld = dt == LCE_BF16 ? cols : round8(cols);
+    s.ld = round64(cols);
     s.part_stride = rows * s.ld;
     off += align256(static_cast<size_t>(s.part_stride) * 2 * (dt == LCE_BF16 ? 1 : 3));
   };
-  if (dt == LCE_F32 && (backward || !few_tokens(N, dt))) {
+  L.copies = (backward || !few_tokens(N, dt)) &&
+             (dt == LCE_F32 || (misaligned(d) && copy_pays(N, width * weights, backward)));
+  if (L.copies) {
     take(L.x, N, d);
     for (int i = 0; i < weights; ++i) take(L.w[i], width, d);
   }
@@ -66,10 +80,14 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
   return L;
 }
 
+// Whether dZ has an array of its own in the workspace.  With no activation dZ is dY: read in place,
+// or copied like the other operands.
+bool own_dz(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t act, lce_dtype_t dt) {
+  return act != LCE_ACT_NONE || dt == LCE_F32 || (misaligned(d_out) && copy_pays(N, d_in, true));
+}
 Layout linear_layout(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t act, bool backward,
                      lce_dtype_t dt) {
-  // with no activation dZ is dY: read in place, or (fp32) split into parts
-  const int nz = backward && (act != LCE_ACT_NONE || dt == LCE_F32) ? 1 : 0;
+  const int nz = backward && own_dz(N, d_in, d_out, act, dt) ? 1 : 0;
   return layout(N, d_in, d_out, 1, nz, backward, dt);
 }
 Layout gated_layout(int64_t N, int64_t d, int64_t F, bool backward, lce_dtype_t dt) {
@@ -86,9 +104,9 @@ struct Call {
   char* ws;
   int num_sms;
   cudaStream_t stream;
-  HeaderState header{};
-  SplitArray split[MAX_SPLIT_ARRAYS];
-  int nsplit = 0;
+  CallState state{};
+  PackArray pack[MAX_PACK_ARRAYS];
+  int npack = 0;
 
   unsigned* flags() const { return reinterpret_cast<unsigned*>(ws); }
   cudaError_t few(int kid, const FfnGemm& g) {
@@ -99,24 +117,23 @@ struct Call {
   }
   cudaError_t tc(int kid, const FfnTc* jobs, int n) {
     return traced(kid, stream,
-                  [&] { return launch_ffn_tc(jobs, n, dt, flags(), &header, num_sms, stream); });
+                  [&] { return launch_ffn_tc(jobs, n, dt, flags(), &state, num_sms, stream); });
   }
-  // x [rows x cols] as an operand of the tensor-core kernel: itself, or its parts in slot s, which
-  // the next split_all() writes
-  FfnOperand operand(const void* x, int64_t ld, int64_t rows, int64_t cols, const Slot& s) {
-    if (dt == LCE_BF16) return FfnOperand{x, rows, cols, ld, 1, 0};
-    split[nsplit++] = SplitArray{static_cast<const float*>(x), ld, rows, cols, ws + s.off, s.ld,
-                                 s.part_stride};
-    return parts(s, rows, cols);
+  // x [rows x cols] as an operand of the tensor-core kernel: itself, or its copy in slot s (if there
+  // is one), which the next pack_all() writes
+  FfnOperand operand(const void* x, int64_t ld, int64_t rows, int64_t cols, const Slot* s) {
+    if (dt == LCE_BF16 && (!s || !misaligned(ld))) return FfnOperand{x, rows, cols, ld, 1, 0};
+    pack[npack++] = PackArray{x, ld, rows, cols, ws + s->off, s->ld, s->part_stride};
+    return own(*s, rows, cols);
   }
-  cudaError_t split_all() {
-    if (nsplit == 0) return cudaSuccess;
-    header.flags = header.sched = true;  // the launch clears the header
-    return traced(K_SPLIT_BF16, stream,
-                  [&] { return launch_split_bf16(split, nsplit, flags(), stream); });
+  cudaError_t pack_all() {
+    if (npack == 0) return cudaSuccess;
+    state.flags = state.sched = state.dependent = true;  // the launch clears the header
+    return traced(K_PACK, stream,
+                  [&] { return launch_pack(pack, npack, dt == LCE_BF16 ? 1 : 3, flags(), stream); });
   }
   // an array of the workspace as an operand
-  FfnOperand parts(const Slot& s, int64_t rows, int64_t cols) const {
+  FfnOperand own(const Slot& s, int64_t rows, int64_t cols) const {
     return FfnOperand{ws + s.off, rows, cols, s.ld, dt == LCE_BF16 ? 1 : 3, s.part_stride};
   }
 };
@@ -197,9 +214,9 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   g.M = N; g.Ncols = d_out; g.K = d_in;
   g.bias = bias; g.R = residual; g.ldr = ldr;
   g.C = Y; g.ldc = ldy;
-  g.A = c.operand(X, ldx, N, d_in, L.x);
-  g.B = c.operand(W, d_in, d_out, d_in, L.w[0]);
-  if (c.split_all() != cudaSuccess || c.tc(K_LIN, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
+  g.A = c.operand(X, ldx, N, d_in, L.copies ? &L.x : nullptr);
+  g.B = c.operand(W, d_in, d_out, d_in, L.copies ? &L.w[0] : nullptr);
+  if (c.pack_all() != cudaSuccess || c.tc(K_LIN, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
   return LCE_OK;
 }
 
@@ -231,11 +248,13 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
   }
   Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   const Layout L = linear_layout(N, d_in, d_out, activation, true, dtype);
-  const FfnOperand x = c.operand(X, ldx, N, d_in, L.x);
-  const FfnOperand w = c.operand(W, d_in, d_out, d_in, L.w[0]);
+  const FfnOperand x = c.operand(X, ldx, N, d_in, L.copies ? &L.x : nullptr);
+  const FfnOperand w = c.operand(W, d_in, d_out, d_in, L.copies ? &L.w[0] : nullptr);
   const bool none = activation == LCE_ACT_NONE;
-  const FfnOperand z = none ? c.operand(dY, ldy, N, d_out, L.z[0]) : c.parts(L.z[0], N, d_out);
-  if (c.split_all() != cudaSuccess) return LCE_ERR_CUDA;
+  const bool own_z = own_dz(N, d_in, d_out, activation, dtype);
+  const FfnOperand z = none ? c.operand(dY, ldy, N, d_out, own_z ? &L.z[0] : nullptr)
+                            : c.own(L.z[0], N, d_out);
+  if (c.pack_all() != cudaSuccess) return LCE_ERR_CUDA;
   if (!none) {
     FfnTc g{};
     g.mode = FFN_LINEAR_DZ;
@@ -248,12 +267,13 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
   }
   if (dbias && traced(K_COLSUM, stream, [&] {
         return launch_column_sum(z.ptr, z.ld, N, d_out, static_cast<int>(z.parts), z.part_stride,
-                                 dbias, stream);
+                                 dbias, c.state.dependent, stream);
       }) != cudaSuccess)
     return LCE_ERR_CUDA;
+  if (dbias) c.state.dependent = true;
   if (products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) != cudaSuccess) return LCE_ERR_CUDA;
   // no launch that clears the error flags (dbias alone, or nothing asked for)
-  if (!c.header.flags && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
+  if (!c.state.flags && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;
   return LCE_OK;
 }
 
@@ -299,10 +319,10 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   g.act = activation;
   g.M = N; g.Ncols = F; g.K = d;
   g.C = H; g.ldc = ldh;
-  g.A = c.operand(X, ldx, N, d, L.x);
-  g.B = c.operand(Wg, d, F, d, L.w[0]);
-  g.B2 = c.operand(Wu, d, F, d, L.w[1]);
-  if (c.split_all() != cudaSuccess || c.tc(K_GATED, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
+  g.A = c.operand(X, ldx, N, d, L.copies ? &L.x : nullptr);
+  g.B = c.operand(Wg, d, F, d, L.copies ? &L.w[0] : nullptr);
+  g.B2 = c.operand(Wu, d, F, d, L.copies ? &L.w[1] : nullptr);
+  if (c.pack_all() != cudaSuccess || c.tc(K_GATED, &g, 1) != cudaSuccess) return LCE_ERR_CUDA;
   return LCE_OK;
 }
 
@@ -333,10 +353,10 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
   }
   Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   const Layout L = gated_layout(N, d, F, true, dtype);
-  const FfnOperand x = c.operand(X, ldx, N, d, L.x);
-  const FfnOperand w[2] = {c.operand(Wg, d, F, d, L.w[0]), c.operand(Wu, d, F, d, L.w[1])};
-  const FfnOperand z[2] = {c.parts(L.z[0], N, F), c.parts(L.z[1], N, F)};
-  if (c.split_all() != cudaSuccess) return LCE_ERR_CUDA;
+  const FfnOperand x = c.operand(X, ldx, N, d, L.copies ? &L.x : nullptr);
+  const FfnOperand w[2] = {c.operand(Wg, d, F, d, L.copies ? &L.w[0] : nullptr), c.operand(Wu, d, F, d, L.copies ? &L.w[1] : nullptr)};
+  const FfnOperand z[2] = {c.own(L.z[0], N, F), c.own(L.z[1], N, F)};
+  if (c.pack_all() != cudaSuccess) return LCE_ERR_CUDA;
   FfnTc g{};
   g.mode = FFN_GATED_DGU;
   g.act = activation;

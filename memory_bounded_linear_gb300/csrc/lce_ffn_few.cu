@@ -3,11 +3,11 @@
 //
 // The weights are read once and little else, so the kernel is a weight stream: bound by HBM.  The
 // tensor cores take the weights as their 128-row operand and the tokens as the columns
-// (D[128 features x NT tokens] = W_tile X^T, NT = 16, 32, 64 or 128, tokens past N zero-filled by
-// TMA), so one kernel serves one token and a hundred at the same bytes.
+// (D[128 features x nt tokens] = W_tile X^T, nt = N rounded up to 16, the tokens past N zero-filled
+// by TMA), so one kernel serves one token and a hundred at the same bytes.
 //   warp 0      TMA producer: k-blocks of 64 of the weight rows (of Wg and Wu both) and of X through
 //               a ring of about 100 KB, two CTAs per SM: 200 KB in flight per SM
-//   warp 1      MMA issuer (tcgen05, cta_group::1, M = 128, N = NT), accumulators in TMEM
+//   warp 1      MMA issuer (tcgen05, cta_group::1, M = 128, N = nt), accumulators in TMEM
 //   warps 2..5  epilogue: thread = feature, so a token's results leave as 64 contiguous bytes a warp
 // With few row tiles the K loop is split over a cluster of S = 2, 4 or 8 CTAs; each puts its fp32
 // partial sums into its shared memory and adds up every S-th token from all of them, in rank order,
@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <algorithm>
 
 #include "lce_act.cuh"
 #include "lce_ffn.h"
@@ -29,25 +31,13 @@ namespace {
 
 constexpr int BK = 64;
 constexpr int THREADS = 192;
-constexpr int RING_BYTES = 110 * 1024;     // two CTAs per SM
-constexpr int WIDE_RING_BYTES = 200 * 1024;  // where the partial sums leave room for one only
 constexpr int MAX_STAGES = 8;
 constexpr int CTL_BYTES = 256;
 constexpr int MAX_SPLIT = 8;
-
-template <int NT, bool GATED>
-struct Cfg {
-  static constexpr int W_BYTES = BM * 128;
-  static constexpr int X_BYTES = NT * 128;
-  static constexpr int STAGE_BYTES = (GATED ? 2 : 1) * W_BYTES + X_BYTES;
-  static constexpr int PART_BYTES = (GATED ? 2 : 1) * NT * BM * 4;  // one CTA's partial sums
-  static constexpr int BUDGET = PART_BYTES <= RING_BYTES ? RING_BYTES : WIDE_RING_BYTES;
-  static constexpr int STAGES = BUDGET / STAGE_BYTES < MAX_STAGES ? BUDGET / STAGE_BYTES : MAX_STAGES;
-  static constexpr int RING = STAGES * STAGE_BYTES > PART_BYTES ? STAGES * STAGE_BYTES : PART_BYTES;
-  static constexpr int SMEM_BYTES = RING + 1024 + CTL_BYTES;
-  static constexpr int COLS = (GATED ? 2 : 1) * NT;
-  static constexpr int TMEM = COLS < 32 ? 32 : COLS;  // a power of two
-};
+constexpr int W_BYTES = BM * 128;  // one k-block of 128 weight rows
+// Shared memory of a CTA (ring or partial sums, alignment, control block) with two or one per SM.
+constexpr int SMEM_TWO = 112 * 1024;
+constexpr int SMEM_ONE = 220 * 1024;
 
 struct Ctl {
   uint64_t full[MAX_STAGES];
@@ -63,7 +53,9 @@ struct Maps {
 };
 
 struct Params {
-  int N, width, nkb, split;
+  int N, nt, width, nkb, split;
+  int stages, stage_bytes, ring_bytes;
+  uint32_t tmem_cols, idesc;
   int act;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* R; int64_t ldr;
@@ -84,15 +76,15 @@ __device__ __forceinline__ void finish(const Params& p, int t, int f, float z, f
   p.Y[t * p.ldy + f] = __float2bfloat16_rn(v);
 }
 
-template <int NT, bool GATED>
+template <bool GATED>
 __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant__ Maps maps,
                                                           const Params p) {
-  using Cf = Cfg<NT, GATED>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_addr);
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + Cf::RING);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + p.ring_bytes);
+  const int x_off = (GATED ? 2 : 1) * W_BYTES;  // X's k-block in a stage
   volatile int* abort_flag = &ctl->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
@@ -103,7 +95,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     // The workspace's error flags: the first CTA is among the first to run, and a wait gives up only
     // WAIT_LIMIT_NS after that.
     if (blockIdx.x == 0) *p.err = 0u;
-    for (int s = 0; s < Cf::STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
     }
@@ -112,7 +104,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), Cf::TMEM);
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), p.tmem_cols);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
@@ -130,12 +122,12 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
           ok = false;
           break;
         }
-        ptx::mbar_arrive_expect_tx(full, Cf::STAGE_BYTES);
-        const uint32_t s0 = base + r.stage * Cf::STAGE_BYTES;
+        ptx::mbar_arrive_expect_tx(full, p.stage_bytes);
+        const uint32_t s0 = base + r.stage * p.stage_bytes;
         ptx::tma_load_2d(s0, &maps.w, kb * BK, tile * BM, full);
-        if (GATED) ptx::tma_load_2d(s0 + Cf::W_BYTES, &maps.w2, kb * BK, tile * BM, full);
-        ptx::tma_load_2d(s0 + Cf::STAGE_BYTES - Cf::X_BYTES, &maps.x, kb * BK, 0, full);
-        if (++r.stage == Cf::STAGES) { r.stage = 0; r.ph ^= 1u; }
+        if (GATED) ptx::tma_load_2d(s0 + W_BYTES, &maps.w2, kb * BK, tile * BM, full);
+        ptx::tma_load_2d(s0 + x_off, &maps.x, kb * BK, 0, full);
+        if (++r.stage == p.stages) { r.stage = 0; r.ph ^= 1u; }
       }
       if (!ok) {  // let copies already in flight land before the CTA can exit
         const uint64_t t0 = ptx::globaltimer();
@@ -144,23 +136,22 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t IDESC = ptx::idesc_bf16_f32(BM, NT, false, false);
       Ring r{0, 0u};
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_bar(ptx::smem_addr(&ctl->full[r.stage]), r.ph, abort_flag, p.err)) break;
         ptx::tc_fence_after();
-        const uint32_t s0 = base + r.stage * Cf::STAGE_BYTES;
-        const uint32_t sx = s0 + Cf::STAGE_BYTES - Cf::X_BYTES;
+        const uint32_t s0 = base + r.stage * p.stage_bytes;
+        const uint32_t sx = s0 + x_off;
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k) {
           const uint32_t acc = (kb != kb0 || k != 0) ? 1u : 0u;
-          ptx::tc_mma_f16(tmem_base, desc_kmajor(s0, k), desc_kmajor(sx, k), IDESC, acc);
+          ptx::tc_mma_f16(tmem_base, desc_kmajor(s0, k), desc_kmajor(sx, k), p.idesc, acc);
           if (GATED)
-            ptx::tc_mma_f16(tmem_base + NT, desc_kmajor(s0 + Cf::W_BYTES, k), desc_kmajor(sx, k),
-                            IDESC, acc);
+            ptx::tc_mma_f16(tmem_base + p.nt, desc_kmajor(s0 + W_BYTES, k), desc_kmajor(sx, k),
+                            p.idesc, acc);
         }
         ptx::tc_commit(ptx::smem_addr(&ctl->empty[r.stage]));
-        if (++r.stage == Cf::STAGES) { r.stage = 0; r.ph ^= 1u; }
+        if (++r.stage == p.stages) { r.stage = 0; r.ph ^= 1u; }
       }
       // the accumulators are complete (after a timeout: no MMA is still writing them)
       ptx::tc_commit(ptx::smem_addr(&ctl->done));
@@ -182,10 +173,10 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     if (p.split == 1) {
       dispatch_act(p.act, [&](auto tag) {
 #pragma unroll 1
-        for (int c = 0; c < NT && c < p.N; c += 16) {
+        for (int c = 0; c < p.N; c += 16) {
           float z[16], u[16];
           ptx::tmem_load16(tbase + c, z);
-          if (GATED) ptx::tmem_load16(tbase + NT + c, u);
+          if (GATED) ptx::tmem_load16(tbase + p.nt + c, u);
           if (f < p.width) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -198,13 +189,14 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
       // every load of the ring has been read by an MMA: its memory holds the partial sums now
       float* part = reinterpret_cast<float*>(smem);
 #pragma unroll 1
-      for (int c = 0; c < NT && c < p.N; c += 16) {
+      for (int c = 0; c < p.N; c += 16) {
         float z[16];
 #pragma unroll
         for (int g = 0; g < (GATED ? 2 : 1); ++g) {
-          ptx::tmem_load16(tbase + g * NT + c, z);
+          ptx::tmem_load16(tbase + g * p.nt + c, z);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(g * NT + c + j) * BM + feature] = z[j];
+          for (int j = 0; j < 16; ++j)
+            if (c + j < p.N) part[(g * p.N + c + j) * BM + feature] = z[j];
         }
       }
     }
@@ -225,7 +217,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
           for (int g = 0; g < (GATED ? 2 : 1); ++g)
 #pragma unroll
             for (int s = 0; s < MAX_SPLIT; ++s)
-              v[g][s] = s < p.split ? ptx::ld_shared_cluster(peer[s] + (g * NT + t) * BM * 4) : 0.f;
+              v[g][s] = s < p.split ? ptx::ld_shared_cluster(peer[s] + (g * p.N + t) * BM * 4) : 0.f;
           float z = 0.f, u = 0.f;
 #pragma unroll
           for (int s = 0; s < MAX_SPLIT; ++s) {
@@ -243,7 +235,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   }
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, Cf::TMEM);
+    ptx::tmem_dealloc(tmem_base, p.tmem_cols);
   }
 }
 
@@ -272,27 +264,22 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int
   return true;
 }
 
-template <int NT, bool GATED>
+template <bool GATED>
 cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
-  using Cf = Cfg<NT, GATED>;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<NT, GATED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
+    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<GATED>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
     if (e != cudaSuccess) {
       set_error_detail("shared-memory attribute of the few-token kernel: %s", cudaGetErrorName(e));
       return e;
     }
     attr_set = true;
   }
-  Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  if (!make_map(&maps.w, g.B, g.K, g.Ncols, g.ldb, BM) ||
-      !make_map(&maps.x, g.A, g.K, g.M, g.lda, NT) ||
-      (GATED && !make_map(&maps.w2, g.B2, g.K, g.Ncols, g.ldb, BM)))
-    return cudaErrorInvalidResourceHandle;
+  constexpr int W = GATED ? 2 : 1;
   Params p{};
   p.N = static_cast<int>(g.M);
+  p.nt = (p.N + 15) / 16 * 16;
   p.width = static_cast<int>(g.Ncols);
   p.nkb = static_cast<int>((g.K + BK - 1) / BK);
   p.act = g.act;
@@ -300,14 +287,37 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   p.R = static_cast<const __nv_bfloat16*>(g.R); p.ldr = g.ldr;
   p.Y = static_cast<__nv_bfloat16*>(g.C); p.ldy = g.ldc;
   p.err = err;
-  // Split K until two CTAs per SM are filled, keeping at least four k-blocks for each.
+  p.idesc = ptx::idesc_bf16_f32(BM, p.nt, false, false);
+  p.tmem_cols = 32;
+  while (p.tmem_cols < static_cast<uint32_t>(W * p.nt)) p.tmem_cols *= 2;
+  p.stage_bytes = W * W_BYTES + p.nt * 128;
+  // Two CTAs per SM while two k-blocks fit in half its shared memory and the accumulators in half its
+  // tensor memory, else one.  (The CTAs an SM holds never need more than its 512 columns together: a
+  // CTA of a cluster that waited for them could be waited for in turn.)
+  const bool two = 2 * p.stage_bytes + 1024 + CTL_BYTES <= SMEM_TWO && p.tmem_cols <= 256;
+  const int budget = (two ? SMEM_TWO : SMEM_ONE) - 1024 - CTL_BYTES;
+  p.stages = std::min(MAX_STAGES, budget / p.stage_bytes);
+  p.ring_bytes = p.stages * p.stage_bytes;
+  // Split K until those places are filled, keeping at least four k-blocks for each CTA and the partial
+  // sums of a tile within the budget.
   const int64_t tiles = (g.Ncols + BM - 1) / BM;
+  const int64_t places = (two ? 2 : 1) * num_sms;
+  const int part_bytes = W * p.N * BM * 4;
   p.split = 1;
-  while (p.split < MAX_SPLIT && tiles * p.split * 2 <= 2 * num_sms && p.nkb >= 8 * p.split) p.split *= 2;
+  while (p.split < MAX_SPLIT && part_bytes <= budget && tiles * p.split * 2 <= places &&
+         p.nkb >= 8 * p.split)
+    p.split *= 2;
+  if (p.split > 1) p.ring_bytes = std::max(p.ring_bytes, part_bytes);
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!make_map(&maps.w, g.B, g.K, g.Ncols, g.ldb, BM) ||
+      !make_map(&maps.x, g.A, g.K, g.M, g.lda, p.nt) ||
+      (GATED && !make_map(&maps.w2, g.B2, g.K, g.Ncols, g.ldb, BM)))
+    return cudaErrorInvalidResourceHandle;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+  cfg.dynamicSmemBytes = p.ring_bytes + 1024 + CTL_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -316,7 +326,7 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<NT, GATED>, maps, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATED>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     set_error_detail("launch of the few-token kernel (%lld tiles, split %d): %s",
@@ -324,19 +334,11 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   return e;
 }
 
-template <bool GATED>
-cudaError_t pick(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
-  if (g.M <= 16) return launch<16, GATED>(g, err, num_sms, stream);
-  if (g.M <= 32) return launch<32, GATED>(g, err, num_sms, stream);
-  if (g.M <= 64) return launch<64, GATED>(g, err, num_sms, stream);
-  return launch<128, GATED>(g, err, num_sms, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
-  return g.mode == FFN_GATED ? pick<true>(g, err, num_sms, stream)
-                             : pick<false>(g, err, num_sms, stream);
+  return g.mode == FFN_GATED ? launch<true>(g, err, num_sms, stream)
+                             : launch<false>(g, err, num_sms, stream);
 }
 
 }  // namespace lce

@@ -1,5 +1,5 @@
 // CUDA-core kernels of the feed-forward operators: fp32 products of a few tokens, column sums
-// (dbias), and the split of fp32 operands into bf16 parts.
+// (dbias), and copies of operands (fp32 into bf16 parts, bf16 into aligned rows).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -122,6 +122,8 @@ __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
                       int64_t cols, O* __restrict__ out) {
   __shared__ float sh[WARPS][SUM_COLS];
   __shared__ float total[SUM_COLS];
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % SUM_SPLIT;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x / SUM_SPLIT) * SUM_COLS;
@@ -177,53 +179,63 @@ __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
   ptx::cluster_sync();  // no block leaves while its sums are read
 }
 
-// ---------------------------------------------------------------------------- bf16 parts
-// Up to MAX_SPLIT_ARRAYS arrays in one launch, bound by memory (4 bytes read, 6 written per element).
-// A block takes SPLIT_VECS groups of four columns of one array; block 0 also clears the workspace
-// header, as the first launch of its call.
-constexpr int SPLIT_UNROLL = 4;
-constexpr int SPLIT_VECS = WARPS * 32 * SPLIT_UNROLL;
+// ---------------------------------------------------------------------------- operand copies
+// Up to MAX_PACK_ARRAYS arrays in one launch, bound by memory: fp32 into three bf16 parts (PARTS = 3,
+// 4 bytes read and 6 written per element) or bf16 into rows of another stride (PARTS = 1).  A block
+// takes PACK_VECS 16-byte groups of one array; block 0 also clears the workspace header, as the first
+// launch of its call.
+constexpr int PACK_UNROLL = 4;
+constexpr int PACK_VECS = WARPS * 32 * PACK_UNROLL;
 
-struct SplitParams {
-  SplitArray a[MAX_SPLIT_ARRAYS];
-  int64_t first[MAX_SPLIT_ARRAYS];  // first block of each array
+struct PackParams {
+  PackArray a[MAX_PACK_ARRAYS];
+  int64_t first[MAX_PACK_ARRAYS];  // first block of each array
   int count;
   unsigned* header;
 };
 
-__global__ void __launch_bounds__(WARPS * 32) split_bf16_kernel(const __grid_constant__ SplitParams p) {
+template <int PARTS>
+__global__ void __launch_bounds__(WARPS * 32) pack_kernel(const __grid_constant__ PackParams p) {
+  constexpr int VEC = PARTS == 3 ? 4 : 8;  // elements per 16 bytes read
+  ptx::launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < WS_HEADER_BYTES / 4) p.header[threadIdx.x] = 0u;
   int k = 0;
   while (k + 1 < p.count && p.first[k + 1] <= blockIdx.x) ++k;
-  const SplitArray& a = p.a[k];
-  const uint32_t c4 = static_cast<uint32_t>(a.cols / 4);
-  const int64_t i0 = (blockIdx.x - p.first[k]) * static_cast<int64_t>(SPLIT_VECS);
-  const int64_t r0 = i0 / c4;
-  const uint32_t o0 = static_cast<uint32_t>(i0 - r0 * c4);  // column group of the block's first
-  float4 v[SPLIT_UNROLL];
-  int64_t row[SPLIT_UNROLL];
-  uint32_t col[SPLIT_UNROLL];
+  const PackArray& a = p.a[k];
+  const uint32_t groups = static_cast<uint32_t>(a.cols / VEC);  // per row
+  const int64_t i0 = (blockIdx.x - p.first[k]) * static_cast<int64_t>(PACK_VECS);
+  const int64_t r0 = i0 / groups;
+  const uint32_t o0 = static_cast<uint32_t>(i0 - r0 * groups);  // group of the block's first
+  uint4 v[PACK_UNROLL];
+  int64_t row[PACK_UNROLL];
+  uint32_t col[PACK_UNROLL];
 #pragma unroll
-  for (int u = 0; u < SPLIT_UNROLL; ++u) {
+  for (int u = 0; u < PACK_UNROLL; ++u) {
     const uint32_t o = o0 + threadIdx.x + u * WARPS * 32;
-    row[u] = r0 + o / c4;
-    col[u] = o % c4 * 4;
-    if (row[u] < a.rows) v[u] = *reinterpret_cast<const float4*>(a.x + row[u] * a.ld + col[u]);
+    row[u] = r0 + o / groups;
+    col[u] = o % groups * VEC;
+    if (row[u] < a.rows)
+      v[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) +
+                                             (row[u] * a.ld + col[u]) * (16 / VEC));
   }
 #pragma unroll
-  for (int u = 0; u < SPLIT_UNROLL; ++u) {
+  for (int u = 0; u < PACK_UNROLL; ++u) {
     if (row[u] >= a.rows) break;
-    float q[4][3];
-    split_bf16(v[u].x, q[0]);
-    split_bf16(v[u].y, q[1]);
-    split_bf16(v[u].z, q[2]);
-    split_bf16(v[u].w, q[3]);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row[u] * a.ld_out + col[u];
+    if constexpr (PARTS == 1) {
+      *reinterpret_cast<uint4*>(out) = v[u];
+    } else {
+      float q[4][3];
+      split_bf16(__uint_as_float(v[u].x), q[0]);
+      split_bf16(__uint_as_float(v[u].y), q[1]);
+      split_bf16(__uint_as_float(v[u].z), q[2]);
+      split_bf16(__uint_as_float(v[u].w), q[3]);
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(q[0][s], q[1][s]),
-                             __floats2bfloat162_rn(q[2][s], q[3][s])};
-      *reinterpret_cast<uint2*>(out + s * a.part_stride) = *reinterpret_cast<uint2*>(h);
+      for (int s = 0; s < 3; ++s) {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(q[0][s], q[1][s]),
+                               __floats2bfloat162_rn(q[2][s], q[3][s])};
+        *reinterpret_cast<uint2*>(out + s * a.part_stride) = *reinterpret_cast<uint2*>(h);
+      }
     }
   }
 }
@@ -235,35 +247,43 @@ cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t str
 }
 
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
-                              int64_t part_stride, void* out, cudaStream_t stream) {
+                              int64_t part_stride, void* out, bool dependent, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((cols + SUM_COLS - 1) / SUM_COLS * SUM_SPLIT);
   const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
-  if (parts == 3)
-    column_sum_kernel<3><<<blocks, WARPS * 32, 0, stream>>>(h, ld, part_stride, N, cols,
-                                                            static_cast<float*>(out));
-  else
-    column_sum_kernel<1><<<blocks, WARPS * 32, 0, stream>>>(h, ld, 0, N, cols,
-                                                            static_cast<__nv_bfloat16*>(out));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(WARPS * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0] = dependent_launch();
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  const cudaError_t e =
+      parts == 3 ? cudaLaunchKernelEx(&cfg, column_sum_kernel<3, float>, h, ld, part_stride, N, cols,
+                                      static_cast<float*>(out))
+                 : cudaLaunchKernelEx(&cfg, column_sum_kernel<1, __nv_bfloat16>, h, ld, int64_t(0), N,
+                                      cols, static_cast<__nv_bfloat16*>(out));
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-cudaError_t launch_split_bf16(const SplitArray* arrays, int count, unsigned* header,
-                              cudaStream_t stream) {
-  if (count < 1 || count > MAX_SPLIT_ARRAYS) return cudaErrorInvalidValue;
-  SplitParams p{};
+cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned* header,
+                        cudaStream_t stream) {
+  if (count < 1 || count > MAX_PACK_ARRAYS || (parts != 1 && parts != 3)) return cudaErrorInvalidValue;
+  PackParams p{};
   p.count = count;
   p.header = header;
   int64_t blocks = 0;
   for (int i = 0; i < count; ++i) {
     p.a[i] = arrays[i];
     p.first[i] = blocks;
-    blocks += (arrays[i].rows * (arrays[i].cols / 4) + SPLIT_VECS - 1) / SPLIT_VECS;
+    blocks += (arrays[i].rows * (arrays[i].cols / (parts == 3 ? 4 : 8)) + PACK_VECS - 1) / PACK_VECS;
   }
   if (blocks > (int64_t(1) << 31) - 1) {
-    set_error_detail("split of %lld blocks: beyond a launch's grid", static_cast<long long>(blocks));
+    set_error_detail("operand copy of %lld blocks: beyond a launch's grid", static_cast<long long>(blocks));
     return cudaErrorInvalidValue;
   }
-  split_bf16_kernel<<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
+  if (parts == 3) pack_kernel<3><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
+  else pack_kernel<1><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

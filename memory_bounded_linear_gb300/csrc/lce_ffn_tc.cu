@@ -359,8 +359,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int unit = static_cast<int>(blockIdx.x >> 1) / split;
 
   if (threadIdx.x == 0) {
-    // the first CTA is among the first to run, and a wait gives up only WAIT_LIMIT_NS after that
-    if (p.clear_flags && blockIdx.x == 0) *p.err = 0u;
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
@@ -384,6 +382,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::tmem_relinquish_pair();
     ptx::tc_fence_before();
   }
+  ptx::launch_dependents();
+  ptx::wait_for_previous();  // the operands may come from the previous launch of this call
+  // the first CTA is among the first to run, and a wait gives up only WAIT_LIMIT_NS after that
+  if (threadIdx.x == 0 && blockIdx.x == 0 && p.clear_flags) *p.err = 0u;
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
@@ -791,7 +793,7 @@ int max_clusters(int pairs) {
 }
 
 template <int MODE, bool F32>
-cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, int num_sms,
+cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, bool dependent, int num_sms,
                    cudaStream_t stream) {
   static bool attr_set = false;
   if (!attr_set) {
@@ -817,13 +819,14 @@ cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, int num_sms,
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2 * p.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1] = dependent_launch();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 2 : 1;
   cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, true>, maps, p)
                               : cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, false>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -834,7 +837,7 @@ cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, int num_sms,
 }
 
 template <bool F32>
-cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, HeaderState* state, int num_sms,
+cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state, int num_sms,
                 cudaStream_t stream) {
   FMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -911,23 +914,26 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, HeaderState* sta
                                       stream);
       if (e != cudaSuccess) return e;
       state->flags = state->sched = true;  // the launch leaves the counters at zero
+      state->dependent = false;
     }
   }
+  const bool dependent = state->dependent;
+  state->dependent = true;
   p.clear_flags = !state->flags;
   state->flags = true;
   switch (mode) {
-    case FFN_LINEAR: return launch<FFN_LINEAR, F32>(maps, p, plan, num_sms, stream);
-    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, plan, num_sms, stream);
-    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, plan, num_sms, stream);
-    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, plan, num_sms, stream);
-    default: return launch<FFN_GRADS, F32>(maps, p, plan, num_sms, stream);
+    case FFN_LINEAR: return launch<FFN_LINEAR, F32>(maps, p, plan, dependent, num_sms, stream);
+    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, plan, dependent, num_sms, stream);
+    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, plan, dependent, num_sms, stream);
+    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, plan, dependent, num_sms, stream);
+    default: return launch<FFN_GRADS, F32>(maps, p, plan, dependent, num_sms, stream);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
-                          HeaderState* state, int num_sms, cudaStream_t stream) {
+                          CallState* state, int num_sms, cudaStream_t stream) {
   if (njobs < 1 || njobs > MAX_JOBS) return cudaErrorInvalidValue;
   return dtype == LCE_BF16 ? run<false>(jobs, njobs, header, state, num_sms, stream)
                            : run<true>(jobs, njobs, header, state, num_sms, stream);

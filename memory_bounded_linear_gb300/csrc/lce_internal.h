@@ -42,14 +42,14 @@ enum Mode : int {
 // the next.  K_TC_GRAD is a strip's gradient alone; K_TC_DHDW its dH and / or dW.
 // K_SPLIT is the tf32 hi / lo split of an fp32 operand (plain or transposed).
 // The feed-forward operators: K_LIN and K_GATED forward, K_LIN_DZ and K_GATED_DGU the gradients of
-// their pre-activations, K_FFN_GRADS dX and / or dW, K_COLSUM dbias, K_SPLIT_BF16 the split of an
-// fp32 operand into bf16 parts.  K_GRAD_NORM and K_GRAD_SCALE are the two passes of clipping.
+// their pre-activations, K_FFN_GRADS dX and / or dW, K_COLSUM dbias, K_PACK copies of
+// operands (fp32 into bf16 parts, or into rows of another stride).  K_GRAD_NORM and K_GRAD_SCALE are the two passes of clipping.
 enum KernelId : int {
   K_TC_FWD = 0, K_TC_BWD = 1,
   K_SIMT_FWD = 2, K_SIMT_BWD_G = 3, K_SIMT_DH = 4, K_SIMT_DW = 5,
   K_COMBINE = 6, K_FINALIZE = 7, K_SPLIT = 8, K_TC_GRAD = 9, K_TC_DHDW = 10,
   K_LIN = 11, K_LIN_DZ = 12, K_GATED = 13, K_GATED_DGU = 14, K_FFN_GRADS = 15, K_COLSUM = 16,
-  K_GRAD_NORM = 17, K_GRAD_SCALE = 18, K_SPLIT_BF16 = 19, K_NUM = 20
+  K_GRAD_NORM = 17, K_GRAD_SCALE = 18, K_PACK = 19, K_NUM = 20
 };
 
 // Operand formats of the tensor-core engine.  OP_BF16: bf16 operands.  OP_TF32X3: fp32 operands
@@ -95,6 +95,16 @@ struct StripArgs {
 
 // Kernels a launcher started beyond its first one (the launch counter adds them), per thread.
 extern thread_local int g_extra_kernels;
+
+// Attribute of a dependent launch: its CTAs may start while the previous kernel of the stream drains,
+// and wait for it (ptx::wait_for_previous) before they touch memory.  Only between kernels of one
+// call, each of which either waits or touches nothing that a running predecessor uses.
+inline cudaLaunchAttribute dependent_launch() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
 
 // Launch bookkeeping (lce_api.cu): trace events around a launch and the launch counter.
 cudaError_t launch_open(cudaStream_t stream, bool* rec);

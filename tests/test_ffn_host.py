@@ -34,7 +34,7 @@ BIG = 1 << 40
 def test_names(lib):
     names = {lib.lce_kernel_name(i).decode() for i in range(11, 20)}
     assert names == {"linear", "linear_dz", "gated", "gated_dg_du", "ffn_grads", "column_sum",
-                     "grad_norm", "grad_scale", "split_bf16"}
+                     "grad_norm", "grad_scale", "pack"}
     assert lib.lce_kernel_name(20) is None
 
 

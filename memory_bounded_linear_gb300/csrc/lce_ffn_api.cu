@@ -29,20 +29,19 @@ bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
 
 // Forward products of at most so many tokens run as a weight stream (lce_ffn_few.cu, and for fp32
 // lce_ffn_simt.cu), larger ones on the kernel whose tiles hold 256 tokens.
-bool few_tokens(int64_t N, lce_dtype_t dt) { return N <= (dt == LCE_BF16 ? FFN_FEW_TOKENS : 32); }
+bool few_tokens(int64_t N, lce_dtype_t dt) { return N <= (dt == LCE_BF16 ? FFN_FEW_TOKENS : 16); }
 
 // Rows of the workspace's arrays start on 128-byte lines.
 int64_t round64(int64_t x) { return (x + 63) & ~int64_t(63); }
 
 // Whether a bf16 operand with rows of `width` elements is copied into aligned rows before the products
-// read it.  Rows that start between 32-byte sectors cost the tensor-core kernel a third of its rate
-// (10240 x 1672 x 3008: 96 us, 1664 wide 68 us); the copy costs a pass over the operand, which pays
-// when every element enters enough products.  Rows whose stride is a multiple of 32 bytes but not
-// of 128 lose 10% and are left alone.
+// read it.  Rows that start between 32-byte sectors cost a K-major operand of the tensor-core kernel a
+// third of its rate (10240 x 1672 x 3008: 96 us, 1664 wide 68 us); the copy costs a pass over the
+// operands, which pays when every element enters enough products (4096 x 4104 x 4096 forward: 99 us
+// with, 116 without; 1024 x 4104 x 4096: 36 with, 32 without).  MN-major operands lose 8% only, and
+// rows whose stride is a multiple of 32 bytes but not of 128 lose 10%: they are left alone.
 bool misaligned(int64_t width) { return width % 16 != 0; }
-bool copy_pays(int64_t N, int64_t width, bool backward) {
-  return N * width >= (backward ? 600 : 1200) * (N + width);
-}
+bool copy_pays(int64_t N, int64_t width) { return N * width >= 1200 * (N + width); }
 
 // One array of the workspace: bf16, or for LCE_F32 three bf16 parts of it.
 struct Slot {
@@ -59,7 +58,9 @@ struct Layout {
   size_t total;
 };
 
-Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool backward,
+// k_major: a product contracts X and the weights over d (the forward pass, or pre-activations that are
+// recomputed).
+Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool backward, bool k_major,
               lce_dtype_t dt) {
   Layout L{};
   size_t off = WS_HEADER_BYTES;
@@ -70,7 +71,7 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
     off += align256(static_cast<size_t>(s.part_stride) * 2 * (dt == LCE_BF16 ? 1 : 3));
   };
   L.copies = (backward || !few_tokens(N, dt)) &&
-             (dt == LCE_F32 || (misaligned(d) && copy_pays(N, width * weights, backward)));
+             (dt == LCE_F32 || (k_major && misaligned(d) && copy_pays(N, width * weights)));
   if (L.copies) {
     take(L.x, N, d);
     for (int i = 0; i < weights; ++i) take(L.w[i], width, d);
@@ -83,15 +84,15 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
 // Whether dZ has an array of its own in the workspace.  With no activation dZ is dY: read in place,
 // or copied like the other operands.
 bool own_dz(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t act, lce_dtype_t dt) {
-  return act != LCE_ACT_NONE || dt == LCE_F32 || (misaligned(d_out) && copy_pays(N, d_in, true));
+  return act != LCE_ACT_NONE || dt == LCE_F32 || (misaligned(d_out) && copy_pays(N, d_in));
 }
 Layout linear_layout(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t act, bool backward,
                      lce_dtype_t dt) {
   const int nz = backward && own_dz(N, d_in, d_out, act, dt) ? 1 : 0;
-  return layout(N, d_in, d_out, 1, nz, backward, dt);
+  return layout(N, d_in, d_out, 1, nz, backward, !backward || act != LCE_ACT_NONE, dt);
 }
 Layout gated_layout(int64_t N, int64_t d, int64_t F, bool backward, lce_dtype_t dt) {
-  return layout(N, d, F, 2, backward ? 2 : 0, backward, dt);
+  return layout(N, d, F, 2, backward ? 2 : 0, backward, true, dt);
 }
 
 cudaError_t zero(void* p, size_t bytes, cudaStream_t stream) {
@@ -354,7 +355,8 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
   Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
   const Layout L = gated_layout(N, d, F, true, dtype);
   const FfnOperand x = c.operand(X, ldx, N, d, L.copies ? &L.x : nullptr);
-  const FfnOperand w[2] = {c.operand(Wg, d, F, d, L.copies ? &L.w[0] : nullptr), c.operand(Wu, d, F, d, L.copies ? &L.w[1] : nullptr)};
+  const FfnOperand w[2] = {c.operand(Wg, d, F, d, L.copies ? &L.w[0] : nullptr),
+                           c.operand(Wu, d, F, d, L.copies ? &L.w[1] : nullptr)};
   const FfnOperand z[2] = {c.own(L.z[0], N, F), c.own(L.z[1], N, F)};
   if (c.pack_all() != cudaSuccess) return LCE_ERR_CUDA;
   FfnTc g{};

@@ -14,17 +14,16 @@ namespace lce {
 namespace {
 
 // ---------------------------------------------------------------- fp32 products of a few tokens
-// Bound by reading the weights once (HBM).  A block computes ROWS features (of Wg and Wu both, when
-// gated) for NT tokens; its eight warps take 512-byte pieces of K in turn, lanes four elements each,
+// Bound by reading the weights once (HBM).  A block computes ROWS features (4; gated 2 of Wg and 2 of
+// Wu) for NT tokens; its eight warps take 512-byte pieces of K in turn, lanes four elements each,
 // and each weight vector loaded serves NT tokens from registers (X comes from L1/L2).  The lanes'
 // sums meet by shuffles, the warps' in shared memory, in a fixed order.
 constexpr int WARPS = 8;
-constexpr int ROWS = 4;
 
 template <int NT, bool GATED>
 __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
                                                              unsigned* err) {
-  constexpr int R = GATED ? 2 * ROWS : ROWS;
+  constexpr int ROWS = GATED ? 2 : 4, R = 4;
   __shared__ float sh[WARPS][R * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0u;  // this kernel never waits
@@ -91,6 +90,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
 
 template <bool GATED>
 cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
+  constexpr int ROWS = GATED ? 2 : 4;
   const unsigned bx = static_cast<unsigned>((g.Ncols + ROWS - 1) / ROWS);
   const auto by = [&](int nt) { return dim3(bx, static_cast<unsigned>((g.M + nt - 1) / nt)); };
   if (g.M == 1) few_f32_kernel<1, GATED><<<by(1), WARPS * 32, 0, stream>>>(g, err);
@@ -101,11 +101,12 @@ cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------- column sums
-// Bound by reading x once.  A cluster of eight blocks takes a strip of 128 columns; warp w of block
-// r sums the rows 8 r + w, 64 + 8 r + w, ... (a row of the strip is 256 contiguous bytes, eight rows
-// in flight), the warps meet in shared memory and the blocks through distributed shared memory, in a
-// fixed order: one launch, no workspace, no atomics.
-constexpr int SUM_COLS = 128;
+// Bound by reading x once; with few columns by how many rows are in flight.  A cluster of eight blocks
+// takes a strip of 64 columns; each half-warp of its 64 warps reads rows of the strip (128 contiguous
+// bytes), eight at a time: 1,024 rows in flight per strip.  Half-warps meet by shuffles, warps in
+// shared memory, blocks through distributed shared memory, in a fixed order: one launch, no
+// workspace, no atomics.
+constexpr int SUM_COLS = 64;
 constexpr int SUM_SPLIT = 8;
 constexpr int SUM_UNROLL = 8;
 
@@ -120,19 +121,19 @@ template <int PARTS, typename O>
 __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
     column_sum_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t part_stride, int64_t N,
                       int64_t cols, O* __restrict__ out) {
-  __shared__ float sh[WARPS][SUM_COLS];
-  __shared__ float total[SUM_COLS];
   ptx::launch_dependents();
   ptx::wait_for_previous();
+  __shared__ float sh[WARPS][SUM_COLS];
+  __shared__ float total[SUM_COLS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % SUM_SPLIT;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x / SUM_SPLIT) * SUM_COLS;
-  const int64_t c = c0 + lane * 4;
+  const int64_t c = c0 + (lane & 15) * 4;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < cols) {
-    constexpr int64_t STEP = SUM_SPLIT * WARPS;
+    constexpr int64_t STEP = SUM_SPLIT * WARPS * 2;
     const int64_t step = STEP * ld;
-    int64_t r = rank * WARPS + warp;
+    int64_t r = (rank * WARPS + warp) * 2 + (lane >> 4);
     const __nv_bfloat16* p = x + r * ld + c;
     for (; r + (SUM_UNROLL - 1) * STEP < N; r += SUM_UNROLL * STEP, p += SUM_UNROLL * step) {
       uint2 q[SUM_UNROLL][PARTS];
@@ -160,7 +161,10 @@ __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sh[warp][lane * 4 + i] = s[i];
+  for (int i = 0; i < 4; ++i) {
+    s[i] += __shfl_xor_sync(0xffffffffu, s[i], 16);
+    if (lane < 16) sh[warp][lane * 4 + i] = s[i];
+  }
   __syncthreads();
   if (threadIdx.x < SUM_COLS) {
     float v = 0.f;

@@ -30,9 +30,11 @@
 // puts its partial sums into its ring's memory, and finishes some of the tile's boxes from all of
 // them, read through distributed shared memory in the order of the pieces.
 //
-// The outgoing gradient D and the residual R enter, and C leaves, through one 4 KB box per epilogue
-// warp (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
-// store.  Six 32 KB stages and eight boxes fill the shared memory.
+// The outgoing gradient D and the residual R enter, and C leaves, through 4 KB boxes of the epilogue
+// warps (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
+// store.  Modes that load boxes have two per warp, both fetched while the products of their tile
+// run, and a ring of five 32 KB stages; the others one box and six stages (with one box the epilogue
+// of 4095 x 2048 -> 8192 took twice the products' time: it waited for each box in turn).
 //
 // Bound: tensor pipe for many tokens.  Ragged edges: TMA zero-fills loads and clips stores.
 #include <cuda.h>
@@ -56,30 +58,49 @@ namespace {
 constexpr int TILE = 256;               // rows and accumulator columns of a pair's tile
 constexpr int HALF = 128;               // B rows per CTA; output columns of a gated tile
 constexpr int BK = 64;                  // K elements per stage (one 128-byte swizzle span)
-constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * 128;
 constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 2 * TILE;
 constexpr int CTL_BYTES = 512;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES + 1024 + CTL_BYTES;
+constexpr int MAX_STAGES = 6;
+constexpr int MAX_BOXES = 2;
+constexpr int FFN_LINEAR_RES = 5;       // FFN_LINEAR with a residual, a kernel of its own
+
+template <int MODE>
+struct Cfg {
+  static constexpr bool GATED = MODE == FFN_GATED || MODE == FFN_GATED_DGU;
+  static constexpr bool DZ = MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU;
+  static constexpr bool LOADS = DZ || MODE == FFN_LINEAR_RES;  // boxes of D or R are loaded
+  static constexpr int BOXES = LOADS ? 2 : 1;                  // per epilogue warp
+  static constexpr int STAGES = LOADS ? 5 : 6;
+  static constexpr int BOX_BYTES = EPI_WARPS * BOXES * STAGE_BUF_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BOX_BYTES + 1024 + CTL_BYTES;
+  static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
+  // a tile's partial sums (SPLIT) fit in the ring
+  static_assert(STAGES * STAGE_BYTES >= TILE * BM * 4, "ring smaller than an accumulator");
+};
 constexpr int RASTER = 8;               // row tiles per rasterisation group (as in lce_tc.cu)
 constexpr int MAX_JOBS = 3;
 constexpr int MAX_SPLIT = 4;             // pairs that may sum one tile: clusters of 8 CTAs
+// Steps that the pieces of a K loop keep at least: of every product of a launch, or else of the long
+// ones only.
+template <bool F32>
+constexpr int MIN_STEPS = F32 ? 1 : 2;
+template <bool F32>
+constexpr int LONG_STEPS = F32 ? 2 : 6;
 constexpr int STATIC_WAVES = 4;         // tiles per pair up to which no scheduler counter is used
 constexpr int F32_STEP = 4;             // k-blocks per accumulator of an fp32 tile
-static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
-
 struct Ctl {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
   uint64_t tq_full[TQ];
   uint64_t tq_empty[TQ];
-  uint64_t box[EPI_WARPS];
+  uint64_t box[EPI_WARPS * MAX_BOXES];
   int tq[TQ];
   uint32_t tmem_base;
   int abort_flag;
@@ -92,13 +113,14 @@ struct Job {
   int pairs;    // operand pairs summed (1 or 2)
   int mn;       // both operands MN-major (dW), else A K-major (and B MN-major in GRADS)
   int c_cols;
+  int whole;    // SPLIT: a cluster sums one tile; else each of its pairs computes a tile of its own
 };
 
 struct KParams {
   Job job[MAX_JOBS];
   int njobs, total_tiles;
+  int planned[MAX_JOBS];   // host: the jobs' places in the plan
   int act;
-  int has_d;               // a box of R or D is loaded
   int split;               // pairs per cluster
   const void* bias;
   int64_t m_rows;          // rows of Z
@@ -121,9 +143,6 @@ struct FMaps {
 // The six part products, smallest first: operand parts of A and B.
 __device__ __forceinline__ int part_a(int s) { return (0x201100 >> (4 * (5 - s))) & 15; }
 __device__ __forceinline__ int part_b(int s) { return (0x021010 >> (4 * (5 - s))) & 15; }
-
-template <int MODE>
-constexpr bool kGated = MODE == FFN_GATED || MODE == FFN_GATED_DGU;
 
 struct TilePos {
   int job, tm, tn;
@@ -156,8 +175,25 @@ __device__ __forceinline__ Range piece_of(int steps, int piece, int split) {
                static_cast<int>(static_cast<int64_t>(steps) * (piece + 1) / split)};
 }
 
+// SPLIT: the work of pair `piece` of cluster `unit`; tm < 0 when there is none.
+__device__ __forceinline__ TilePos locate_split(const KParams& p, int unit, int piece) {
+  int j = 0;
+  while (true) {
+    const Job& jb = p.job[j];
+    const int clusters = jb.whole ? jb.num_tiles : (jb.num_tiles + p.split - 1) / p.split;
+    if (j + 1 == p.njobs || unit < clusters) break;
+    unit -= clusters;
+    ++j;
+  }
+  const int tile = p.job[j].whole ? unit : unit * p.split + piece;
+  TilePos r{j, -1, -1};
+  if (tile < p.job[j].num_tiles)
+    tile_coords(tile, p.job[j].tiles_m, p.job[j].tiles_n, RASTER, r.tm, r.tn);
+  return r;
+}
+
 // Producer side of one tile.  A_MN, B_MN: the operand is MN-major.
-template <bool A_MN, bool B_MN, bool F32>
+template <bool A_MN, bool B_MN, bool F32, int STAGES>
 __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, const CUtensorMap* mA,
                                              const CUtensorMap* mB, int m0, int n0, uint32_t base,
                                              Ctl* ctl, Ring& r, volatile int* abort_flag,
@@ -204,7 +240,7 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, co
   return true;
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, int STAGES>
 __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t base, Ctl* ctl, Ring& r,
                                          volatile int* abort_flag, unsigned* err, uint16_t pair_mask) {
   constexpr uint32_t IDESC = ptx::idesc_bf16_f32(TILE, TILE, A_MN, B_MN);
@@ -262,14 +298,15 @@ __device__ __forceinline__ uint4 pack(const float* v) {
 // and the dU values in z; for fp32 pre-activation gradients both stay in registers (z, u).
 template <int MODE, int ACT, bool F32>
 __device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint32_t row, uint32_t sw,
-                                           int first, int col, int c_cols, const void* bias,
-                                           bool has_d) {
+                                           int first, int col, int c_cols, const void* bias) {
   constexpr int CH = CHUNK<F32>;
+  constexpr bool LINEAR = MODE == FFN_LINEAR || MODE == FFN_LINEAR_RES;
+  constexpr bool DZ = Cfg<MODE>::DZ;
 #pragma unroll
   for (int q = 0; q < 32 / CH; ++q) {
     const uint32_t addr = row + ((static_cast<uint32_t>(first + q) ^ sw) << 4);
     float d[CH], o[CH], b[CH];
-    if ((MODE == FFN_LINEAR || MODE == FFN_LINEAR_DZ)) {
+    if (LINEAR || MODE == FFN_LINEAR_DZ) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) b[i] = 0.f;
       if (bias != nullptr && col + q * CH < c_cols) {
@@ -278,16 +315,15 @@ __device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint3
         unpack<F32>(__ldg(reinterpret_cast<const uint4*>(pb)), b);
       }
     }
-    const bool read = MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU || (MODE == FFN_LINEAR && has_d);
-    if (read) unpack<F32>(ptx::ld_shared_v4(addr), d);
+    if (Cfg<MODE>::LOADS) unpack<F32>(ptx::ld_shared_v4(addr), d);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const float v = z[q * CH + i];
       if constexpr (MODE == FFN_GRADS) {
         o[i] = v;
-      } else if constexpr (MODE == FFN_LINEAR) {
+      } else if constexpr (LINEAR) {
         o[i] = act<ACT, !F32>(v + b[i]);
-        if (has_d) o[i] += d[i];
+        if (MODE == FFN_LINEAR_RES) o[i] += d[i];
       } else if constexpr (MODE == FFN_GATED) {
         o[i] = act<ACT, !F32>(v) * u[q * CH + i];
       } else {
@@ -303,48 +339,60 @@ __device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint3
         }
       }
     }
-    if (!(F32 && (MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU))) {
+    if (!(F32 && DZ)) {
       const uint4 w = pack<F32>(o);
       ptx::st_shared_v4(addr, w.x, w.y, w.z, w.w);
     }
   }
 }
 
-// fp32 values of one row as three bf16 parts, 64 bytes per part.
-__device__ __forceinline__ void store_parts(const float (&v)[32], __nv_bfloat16* out, int64_t stride,
-                                            int cols) {
+// 32 columns of a warp's 32 rows, fp32 values of one row per thread, as three bf16 parts: through
+// `stage` (2 KB of shared memory, 64-byte rows with their 16-byte chunks rotated against bank
+// conflicts), so that four lanes write a row's 64 bytes together.  rows, cols: what exists of the box;
+// the padding of a row to a multiple of 8 columns may be written, nothing reads it.
+__device__ __forceinline__ void store_parts(const float (&v)[32], uint32_t stage, __nv_bfloat16* out,
+                                            int64_t ld, int64_t stride, int64_t rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[3][16];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[3][4];
+  for (int i = 0; i < 16; ++i) {
+    float a[3], b[3];
+    split_bf16(v[2 * i], a);
+    split_bf16(v[2 * i + 1], b);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) w[s][i] = pack2(a[s], b[s]);
+  }
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      ptx::st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[s][4 * c], w[s][4 * c + 1],
+                        w[s][4 * c + 2], w[s][4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float p[2][3];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) split_bf16(v[q * 8 + 2 * i + e], p[e]);
-#pragma unroll
-      for (int s = 0; s < 3; ++s) w[s][i] = pack2(p[0][s], p[1][s]);
-    }
-    // the row's padding to a multiple of 8 columns may be written: nothing reads it
-    if (q * 8 < cols) {
-#pragma unroll
-      for (int s = 0; s < 3; ++s)
-        *reinterpret_cast<uint4*>(out + s * stride + q * 8) =
-            make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+      const int r = i * 8 + (lane >> 2);
+      const uint4 x = ptx::ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      if (r < rows && c * 8 < cols) *reinterpret_cast<uint4*>(out + s * stride + r * ld + c * 8) = x;
     }
   }
+  __syncwarp();
 }
 
 template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     ffn_tc_kernel(const __grid_constant__ FMaps maps, const KParams p) {
-  constexpr bool GATED = kGated<MODE>;
-  constexpr bool DZ = MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU;
+  using Cf = Cfg<MODE>;
+  constexpr bool GATED = Cf::GATED, DZ = Cf::DZ;
+  constexpr int STAGES = Cf::STAGES, BOXES = Cf::BOXES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;  // 128B-swizzled tiles need 1024B alignment
   uint8_t* smem = smem_raw + (base - raw_addr);
   const uint32_t boxes = base + STAGES * STAGE_BYTES;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES + Cf::BOX_BYTES);
   volatile int* abort_flag = &ctl->abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -373,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // readers: MMA issuer, the second CTA's producer, the epilogue warps of both
       ptx::mbar_init(ptx::smem_addr(&ctl->tq_empty[i]), 2 + 2 * EPI_WARPS);
     }
-    for (int i = 0; i < EPI_WARPS; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->box[i]), 1);
+    for (int i = 0; i < EPI_WARPS * BOXES; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->box[i]), 1);
     ctl->abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -381,6 +429,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base), TMEM_COLS);
     ptx::tmem_relinquish_pair();
     ptx::tc_fence_before();
+  }
+  if (warp == 0 && lane == 0) {
+    for (int j = 0; j < p.njobs; ++j) {
+      ptx::prefetch_tmap(&maps.a[j][0]);
+      ptx::prefetch_tmap(&maps.b[j][0]);
+    }
   }
   ptx::launch_dependents();
   ptx::wait_for_previous();  // the operands may come from the previous launch of this call
@@ -390,36 +444,35 @@ __global__ void __launch_bounds__(THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
 
-  // Epilogue warps: the warp's box, and the work on one box of results.
+  // Epilogue warps: the warp's boxes, and the work on one box of results.
   const int e = (warp + 6) & 7;  // warps 2..9
   const int q = warp & 3;        // TMEM lane quadrant the warp may access
   const int half = e >> 2;       // which half of the columns it drains
   constexpr int UC = F32 ? 32 : 64;          // columns of one box
   constexpr int COLS = GATED ? HALF : TILE;  // output columns of a tile
   constexpr int UNITS = COLS / 2 / UC;       // boxes per warp and tile
-  const uint32_t box = boxes + e * STAGE_BUF_BYTES;
-  const uint32_t box_bar = ptx::smem_addr(&ctl->box[e]);
-  const uint32_t row_addr = box + lane * 128, sw = lane & 7;
-  const bool has_d = DZ || (MODE == FFN_LINEAR && p.has_d);
-  uint32_t box_ph = 0;
-  bool in_flight = false;
-  int split_tile = -1;
-  // R or D into the box, once the store before it has been read
-  auto fetch = [&](int col, int box_row) {
+  const uint32_t my_boxes = boxes + e * BOXES * STAGE_BUF_BYTES;
+  const uint32_t sw = lane & 7;
+  uint32_t box_ph = 0, in_flight = 0;  // a bit per box
+  int split_tile = -1;                 // SPLIT: the cluster whose tile is finished together
+  auto box_bar = [&](int i) { return ptx::smem_addr(&ctl->box[e * BOXES + i]); };
+  // R or D of one box of results into box i, once the stores from the boxes have been read
+  auto fetch = [&](int i, int col, int box_row) {
     if (lane == 0) {
       ptx::bulk_wait_read<0>();
-      ptx::mbar_arrive_expect_tx(box_bar, STAGE_BUF_BYTES);
-      ptx::tma_load_2d(box, &maps.d, col, box_row, box_bar);
+      ptx::mbar_arrive_expect_tx(box_bar(i), STAGE_BUF_BYTES);
+      ptx::tma_load_2d(my_boxes + i * STAGE_BUF_BYTES, &maps.d, col, box_row, box_bar(i));
     }
-    in_flight = true;
+    in_flight |= 1u << i;
   };
-  // One box of results: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32 accumulator
-  // columns of the thread's row.  False when a wait gave up.
-  auto process = [&](const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load) {
-    if (has_d) {
-      if (!wait_bar(box_bar, box_ph, abort_flag, p.err)) return false;
-      in_flight = false;
-      box_ph ^= 1u;
+  // One box of results through box i: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32
+  // accumulator columns of the thread's row.  False when a wait gave up.
+  auto process = [&](int i, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load) {
+    const uint32_t box = my_boxes + i * STAGE_BUF_BYTES, row_addr = box + lane * 128;
+    if (Cf::LOADS) {
+      if (!wait_bar(box_bar(i), (box_ph >> i) & 1u, abort_flag, p.err)) return false;
+      in_flight &= ~(1u << i);
+      box_ph ^= 1u << i;
     } else {
       if (lane == 0) ptx::bulk_wait_read<0>();
       __syncwarp();
@@ -430,51 +483,47 @@ __global__ void __launch_bounds__(THREADS, 1)
       float z[32], u[32];
       load(h, z, u);
       if constexpr (MODE == FFN_GRADS)
-        epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols, nullptr,
-                                            false);
+        epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols, nullptr);
       else
         dispatch_act(p.act, [&](auto tag) {
           epilogue32<MODE, decltype(tag)::value, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols,
-                                                      p.bias, has_d);
+                                                      p.bias);
         });
       if constexpr (MODE == FFN_GATED_DGU && !F32) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) keep[h * 16 + i] = pack2(z[2 * i], z[2 * i + 1]);
+        for (int k = 0; k < 16; ++k) keep[h * 16 + k] = pack2(z[2 * k], z[2 * k + 1]);
       }
       if constexpr (DZ && F32) {
-        const int64_t row = box_row + lane;
-        if (row < p.m_rows) {
-          const int64_t off = row * p.part_ld + col;
-          store_parts(z, p.parts[0] + off, p.part_stride, c_cols - col);
-          if (GATED) store_parts(u, p.parts[1] + off, p.part_stride, c_cols - col);
-        }
+        // the box has been read: it stages the parts
+        const int64_t off = box_row * p.part_ld + col;
+        store_parts(z, box, p.parts[0] + off, p.part_ld, p.part_stride, p.m_rows - box_row, c_cols - col);
+        if (GATED)
+          store_parts(u, box, p.parts[1] + off, p.part_ld, p.part_stride, p.m_rows - box_row,
+                      c_cols - col);
       }
     }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     if constexpr (!(DZ && F32)) {
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
       if (lane == 0) {
         ptx::tma_store_2d(mC, box, col, box_row);
         ptx::bulk_commit();
       }
       if constexpr (MODE == FFN_GATED_DGU) {
-        if (lane == 0) ptx::bulk_wait_read<0>();
-        __syncwarp();
+        // dU through the other box, which a bf16 tile loads nothing into
+        static_assert(F32 || UNITS == 1, "one box of D per warp and tile");
+        const uint32_t row2 = my_boxes + (i ^ 1) * STAGE_BUF_BYTES + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          ptx::st_shared_v4(row_addr + ((static_cast<uint32_t>(c) ^ sw) << 4), keep[4 * c],
-                            keep[4 * c + 1], keep[4 * c + 2], keep[4 * c + 3]);
+          ptx::st_shared_v4(row2 + ((static_cast<uint32_t>(c) ^ sw) << 4), keep[4 * c], keep[4 * c + 1],
+                            keep[4 * c + 2], keep[4 * c + 3]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          ptx::tma_store_2d(&maps.c2, box, col, box_row);
+          ptx::tma_store_2d(&maps.c2, my_boxes + (i ^ 1) * STAGE_BUF_BYTES, col, box_row);
           ptx::bulk_commit();
         }
       }
-    } else {
-      // every lane has read its row before the next box may land on it
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
     }
     return true;
   };
@@ -507,28 +556,31 @@ __global__ void __launch_bounds__(THREADS, 1)
           tile = tq.take(1u);
         }
         if (tile < 0) break;
-        const TilePos tp = locate(p, tile);
+        const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
+        if (SPLIT && tp.tm < 0) continue;
         const Job& jb = p.job[tp.job];
+        const bool whole = SPLIT && jb.whole;
         const int m0 = tp.tm * TILE + static_cast<int>(rank) * BM;
-        const Range range = piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, piece, split);
+        const Range range =
+            piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, whole ? piece : 0, whole ? split : 1);
         if constexpr (GATED) {
           // CTA 0 loads its columns' rows of Wg, CTA 1 the same rows of Wu
-          ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
+          ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
                                                tp.tn * HALF, base, ctl, ring, abort_flag, p.err,
                                                rank, leader);
         } else {
           const int n0 = tp.tn * TILE + static_cast<int>(rank) * HALF;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = produce_tile<true, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+              ok = produce_tile<true, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                  maps.b[tp.job], m0, n0, base, ctl, ring, abort_flag,
                                                  p.err, rank, leader);
             else
-              ok = produce_tile<false, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+              ok = produce_tile<false, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                   maps.b[tp.job], m0, n0, base, ctl, ring,
                                                   abort_flag, p.err, rank, leader);
           } else {
-            ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
+            ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
                                                  ctl, ring, abort_flag, p.err, rank, leader);
           }
         }
@@ -550,10 +602,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (ok) {
         const int tile = tq.take(1u);
         if (tile < 0) break;
-        const TilePos tp = locate(p, tile);
+        const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
+        if (SPLIT && tp.tm < 0) continue;
         const Job& jb = p.job[tp.job];
+        const bool whole = SPLIT && jb.whole;
         const int per_pair = steps_per_pair<F32>(jb.nkb);
-        const Range range = piece_of(per_pair * jb.pairs, piece, split);
+        const Range range = piece_of(per_pair * jb.pairs, whole ? piece : 0, whole ? split : 1);
         for (int st = range.lo; ok && (st < range.hi || st == range.lo); ++st) {
           // an empty piece still hands its accumulator over; no one reads it
           const int blocks = range.hi == range.lo ? 0
@@ -567,11 +621,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t d_tmem = tmem_base + acc * TILE;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+              ok = mma_tile<true, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
             else
-              ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+              ok = mma_tile<false, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
           } else {
-            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+            ok = mma_tile<false, false, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
           }
           if (!ok) break;
           ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), pair_mask);
@@ -595,14 +649,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (ok) {
       const int tile = tq.take(0xffffffffu);
       if (tile < 0) break;
-      const TilePos tp = locate(p, tile);
+      const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
+      if (SPLIT && tp.tm < 0) continue;
       const Job& jb = p.job[tp.job];
+      const bool whole = SPLIT && jb.whole;
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      const Range range = piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, piece, split);
+      const Range range =
+          piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, whole ? piece : 0, whole ? split : 1);
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
       const int col0 = tp.tn * COLS + half * (COLS / 2);
-      // R or D of the first box, while the products run
-      if (!SPLIT && has_d && col0 < jb.c_cols) fetch(col0, box_row);
+      // the n-th box of this warp: its first column.  Boxes of a tile that a cluster finishes together:
+      // box b belongs to pair b % split, there to the warps of column half (b / split) % 2.
+      auto box_col = [&](int n) {
+        return whole ? tp.tn * COLS + (piece + split * (half + 2 * n)) * UC : col0 + n * UC;
+      };
+      const int col_end = min(jb.c_cols, (tp.tn + 1) * COLS);
+      if (Cf::LOADS) {  // R or D of the first boxes, while the products run
+        for (int n = 0; n < min(BOXES, UNITS); ++n)
+          if (box_col(n) < col_end) fetch(n, box_col(n), box_row);
+      }
       // hand the accumulator back to the MMA issuer (in the pair's first CTA)
       auto release = [&]() {
         ptx::tc_fence_before();
@@ -637,36 +702,39 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       ptx::tc_fence_after();
       const uint32_t tbase = lanes + acc * TILE;
-      if constexpr (SPLIT) {
-        // This pair's partial sums into shared memory, [column][row]: every MMA is done, so the ring
-        // is free.  A cluster computes one tile: the boxes follow below, once all pairs are here.
+      if (whole) {
+        // This pair's partial sums into shared memory, four columns of a row together: every MMA is
+        // done, so the ring is free.  The boxes follow below, once all pairs are here.
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           const int c = half_col<GATED>(half, h);
           float v[32];
           ptx::tmem_load32(tbase + c, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            ptx::st_shared_f32(base + ((c + i) * BM + q * 32 + lane) * 4, v[i]);
+          for (int i = 0; i < 32; i += 4)
+            ptx::st_shared_v4(base + (((c + i) >> 2) * BM + q * 32 + lane) * 16, __float_as_uint(v[i]),
+                              __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                              __float_as_uint(v[i + 3]));
         }
-        release();
         split_tile = tile;
       } else {
 #pragma unroll 1
         for (int un = 0; un < UNITS; ++un) {
           const int col = col0 + un * UC;
-          if (col >= jb.c_cols) break;  // same for every thread of the warp
-          if (has_d && un > 0) fetch(col, box_row);
+          if (col >= col_end) break;  // same for every thread of the warp
           const int at = half * (COLS / 2) + un * UC;  // accumulator column
-          ok = process(&maps.c[tp.job], jb.c_cols, col, box_row, [&](int h, float (&z)[32], float (&u)[32]) {
-            ptx::tmem_load32(tbase + at + h * 32, z);
-            if (GATED) ptx::tmem_load32(tbase + HALF + at + h * 32, u);
-          });
+          ok = process(un % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
+                       [&](int h, float (&z)[32], float (&u)[32]) {
+                         ptx::tmem_load32(tbase + at + h * 32, z);
+                         if (GATED) ptx::tmem_load32(tbase + HALF + at + h * 32, u);
+                       });
           if (!ok) break;
+          if (Cf::LOADS && un + BOXES < UNITS && col + BOXES * UC < col_end)
+            fetch(un % BOXES, col + BOXES * UC, box_row);
         }
         if (!ok) break;
-        release();
       }
+      release();
     }
   }
 
@@ -674,40 +742,57 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     ptx::cluster_sync();  // every pair's partial sums are written
     if (warp >= 2 && split_tile >= 0) {
-      const TilePos tp = locate(p, split_tile);
+      const TilePos tp = locate_split(p, split_tile, piece);
       const Job& jb = p.job[tp.job];
       const int steps = steps_per_pair<F32>(jb.nkb) * jb.pairs;
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
-      // box b is finished by pair b % split, its warps of column half (b / split) % 2
-#pragma unroll 1
-      for (int b = piece; b < COLS / UC; b += split) {
-        if (((b / split) & 1) != half) continue;
-        const int col = tp.tn * COLS + b * UC;
-        if (col >= jb.c_cols) break;
-        if (has_d) fetch(col, box_row);
-        const bool ok = process(&maps.c[tp.job], jb.c_cols, col, box_row, [&](int h, float (&z)[32], float (&u)[32]) {
+      const int col_end = min(jb.c_cols, (tp.tn + 1) * COLS);
+      // 32 columns from all pairs, in the order of the pieces
+      auto gather = [&](int c, float (&v)[32]) {
+        const uint32_t at = base + ((c >> 2) * BM + q * 32 + lane) * 16;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = u[i] = 0.f;
-          const uint32_t at = base + ((b * UC + h * 32) * BM + q * 32 + lane) * 4;
-#pragma unroll 1
-          for (int s = 0; s < split; ++s) {  // in the order of the pieces
+        for (int g = 0; g < 2; ++g) {
+          float4 t[MAX_SPLIT][4];
+#pragma unroll
+          for (int s = 0; s < MAX_SPLIT; ++s) {
             const Range r = piece_of(steps, s, split);
-            if (r.lo == r.hi) continue;
-            const uint32_t peer = ptx::mapa_shared(at, 2 * s + rank);
+            const bool some = s < split && r.lo < r.hi;
+            const uint32_t peer = ptx::mapa_shared(at + g * 4 * BM * 16, some ? 2 * s + rank : crank);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] += ptx::ld_shared_cluster(peer + i * BM * 4);
-            if (GATED) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] += ptx::ld_shared_cluster(peer + (HALF + i) * BM * 4);
-            }
+            for (int i = 0; i < 4; ++i)
+              t[s][i] = some ? ptx::ld_shared_cluster_v4(peer + i * BM * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
-        });
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4 x = t[0][i];
+#pragma unroll
+            for (int s = 1; s < MAX_SPLIT; ++s) {
+              x.x += t[s][i].x; x.y += t[s][i].y; x.z += t[s][i].z; x.w += t[s][i].w;
+            }
+            v[g * 16 + 4 * i] = x.x; v[g * 16 + 4 * i + 1] = x.y;
+            v[g * 16 + 4 * i + 2] = x.z; v[g * 16 + 4 * i + 3] = x.w;
+          }
+        }
+      };
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        const int b = piece + split * (half + 2 * n);
+        const int col = tp.tn * COLS + b * UC;
+        if (col >= col_end) break;
+        const bool ok = process(n % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
+                                [&](int h, float (&z)[32], float (&u)[32]) {
+                                  gather(b * UC + h * 32, z);
+                                  if (GATED) gather(HALF + b * UC + h * 32, u);
+                                });
         if (!ok) break;
+        const int next = col + BOXES * 2 * split * UC;
+        if (Cf::LOADS && next < col_end) fetch(n % BOXES, next, box_row);
       }
     }
   }
   if (warp >= 2) {
-    if (in_flight) wait_bar_drain(box_bar, box_ph, 100000000ull);
+    for (int i = 0; i < BOXES; ++i)
+      if ((in_flight >> i) & 1u) wait_bar_drain(box_bar(i), (box_ph >> i) & 1u, 100000000ull);
     if (lane == 0) ptx::bulk_wait<0>();  // this warp's output stores have landed
     __syncwarp();
   }
@@ -763,7 +848,8 @@ bool operand(CUtensorMap* m, const FfnOperand& o, bool mn, const char* what) {
 // What decides how a launch's sums are cut: all its products, asked for or not, so that a result is
 // the same bits whichever others are computed with it.
 struct Plan {
-  int tiles, longest;  // tiles, and steps of the longest K loop
+  int n;
+  int tiles[MAX_JOBS], steps[MAX_JOBS];  // of each product; steps of its K loop
 };
 
 // Largest grid, in clusters of `pairs` CTA pairs, that the device holds at once (0: unknown).
@@ -774,7 +860,7 @@ int max_clusters(int pairs) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.dynamicSmemBytes = Cfg<MODE>::SMEM_BYTES;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * pairs;
@@ -798,26 +884,48 @@ cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, bool depende
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MODE>::SMEM_BYTES);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MODE>::SMEM_BYTES);
     if (e != cudaSuccess) {
       set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(e));
       return e;
     }
     attr_set = true;
   }
-  // Few tiles: each is summed by 2 or 4 pairs, as long as all clusters run at once and the longest
-  // K loop leaves every pair at least 8 k-blocks.
+  // Few tiles: each is summed by 2 or 4 pairs, as long as all clusters run at once.  Where that does
+  // not fit for every product of the launch, only those with a long K loop are cut and the pairs of a
+  // cluster take tiles of the others side by side.
   p.split = 1;
-  for (int k = 2; k <= MAX_SPLIT; k *= 2)
-    if (plan.longest >= (F32 ? 2 : 8) * k && plan.tiles <= max_clusters<MODE, F32>(k)) p.split = k;
+  bool whole[MAX_JOBS] = {};
+  for (int k = 2; k <= MAX_SPLIT; k *= 2) {
+    for (int least = MIN_STEPS<F32>; least <= LONG_STEPS<F32>; least = least < LONG_STEPS<F32> ? LONG_STEPS<F32> : least + 1) {
+      int64_t clusters = 0;
+      bool any = false;
+      for (int j = 0; j < plan.n; ++j) {
+        const bool w = plan.steps[j] >= least * k;
+        any |= w;
+        clusters += w ? plan.tiles[j] : (plan.tiles[j] + k - 1) / k;
+      }
+      if (!any || clusters > max_clusters<MODE, F32>(k)) continue;
+      p.split = k;
+      for (int j = 0; j < plan.n; ++j) whole[j] = plan.steps[j] >= least * k;
+      break;
+    }
+  }
+  int clusters = 0;
+  for (int j = 0; j < p.njobs; ++j) {
+    Job& jb = p.job[j];
+    jb.whole = p.split > 1 && whole[p.planned[j]];
+    clusters += jb.whole ? jb.num_tiles : (jb.num_tiles + p.split - 1) / p.split;
+  }
   const int units = num_sms / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (p.split > 1 ? p.total_tiles * p.split : std::min(p.total_tiles, units)), 1, 1);
+  if (p.split > 1) p.total_tiles = clusters;  // a ticket is a cluster's work
+  cfg.gridDim = dim3(2 * (p.split > 1 ? clusters * p.split : std::min(p.total_tiles, units)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = Cfg<MODE>::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -846,7 +954,8 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   const bool gated = mode == FFN_GATED || mode == FFN_GATED_DGU;
   const bool dz = mode == FFN_LINEAR_DZ || mode == FFN_GATED_DGU;
   const uint32_t uc = F32 ? 32 : 64;
-  Plan plan{0, 0};
+  Plan plan{};
+  int64_t all_tiles = 0;
   int n = 0;
   for (int i = 0; i < njobs; ++i) {
     const FfnTc& g = jobs[i];
@@ -854,7 +963,7 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
     const int64_t cols = gated ? HALF : TILE;
     const int64_t tm = (g.M + TILE - 1) / TILE, tn = (g.Ncols + cols - 1) / cols;
     const int64_t nkb = (g.K + BK - 1) / BK;
-    if (tm * tn > (int64_t(1) << 28) || plan.tiles + tm * tn > (int64_t(1) << 29) || nkb > (1 << 25)) {
+    if (tm * tn > (int64_t(1) << 28) || all_tiles + tm * tn > (int64_t(1) << 29) || nkb > (1 << 25)) {
       set_error_detail("feed-forward product of %lld x %lld tiles: beyond the scheduler's range",
                        static_cast<long long>(tm), static_cast<long long>(tn));
       return cudaErrorInvalidValue;
@@ -866,11 +975,13 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
     jb.pairs = (!gated && g.A2.ptr) ? 2 : 1;
     jb.mn = g.a_mn;
     jb.c_cols = static_cast<int>(g.Ncols);
-    plan.tiles += jb.num_tiles;
-    plan.longest = std::max(plan.longest, steps_per_pair<F32>(jb.nkb) * jb.pairs);
+    all_tiles += jb.num_tiles;
+    plan.tiles[plan.n] = jb.num_tiles;
+    plan.steps[plan.n++] = steps_per_pair<F32>(jb.nkb) * jb.pairs;
     if (!g.C) continue;  // a result that is not asked for counts in the plan only
     const int j = n++;
     p.job[j] = jb;
+    p.planned[j] = plan.n - 1;
     p.total_tiles += jb.num_tiles;
     if (!operand(&maps.a[j][0], g.A, g.a_mn, "A") || !operand(&maps.b[j][0], g.B, g.b_mn, "B"))
       return cudaErrorInvalidResourceHandle;
@@ -893,7 +1004,6 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   p.bias = g.bias;
   p.m_rows = g.M;
   const void* d = dz ? g.D : (mode == FFN_LINEAR ? g.R : nullptr);
-  p.has_d = d != nullptr;
   if (d && !make_map(&maps.d, d, g.Ncols, g.M, dz ? g.ldd : g.ldr, uc, 32, F32, 2, 1, 0, "D"))
     return cudaErrorInvalidResourceHandle;
   if (dz && F32) {
@@ -922,7 +1032,9 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   p.clear_flags = !state->flags;
   state->flags = true;
   switch (mode) {
-    case FFN_LINEAR: return launch<FFN_LINEAR, F32>(maps, p, plan, dependent, num_sms, stream);
+    case FFN_LINEAR:
+      return d ? launch<FFN_LINEAR_RES, F32>(maps, p, plan, dependent, num_sms, stream)
+               : launch<FFN_LINEAR, F32>(maps, p, plan, dependent, num_sms, stream);
     case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, plan, dependent, num_sms, stream);
     case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, plan, dependent, num_sms, stream);
     case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, plan, dependent, num_sms, stream);

@@ -1,7 +1,8 @@
 // Feed-forward products on the tensor cores of sm_103a (tcgen05 + TMEM + TMA).
 //
-// One persistent, warp-specialised kernel on CTA pairs; a pair computes a 256 x 256 tile of
-// accumulators with cta_group::2 MMAs, CTA r holding its rows 128 r .. 128 r + 127:
+// One persistent, warp-specialised kernel on CTA pairs; a pair computes a tile of 256 x bn
+// accumulators (bn = 256, or 128 for small products) with cta_group::2 MMAs, CTA r holding its rows
+// 128 r .. 128 r + 127:
 //   warp 0      TMA producer and tile scheduler (as in lce_tc.cu)
 //   warp 1      MMA issuer; two 128 x 256 fp32 accumulators in TMEM, one filled while the other
 //               is drained
@@ -10,10 +11,10 @@
 // Modes (FfnMode):
 //   LINEAR     C = act(Z + bias) + R            Z = A B^T, operands K-major
 //   LINEAR_DZ  C = D act'(Z + bias)
-//   GATED      C = act(G) U                     the pair's first CTA loads 128 rows of Wg, the second
-//   GATED_DGU  C = D U act'(G), C2 = D act(G)   the same 128 rows of Wu: the 256 accumulator columns
-//                                               are G | U of 128 output columns, and one thread
-//                                               holds both values of an element
+//   GATED      C = act(G) U                     the pair's first CTA loads bn/2 rows of Wg, the second
+//   GATED_DGU  C = D U act'(G), C2 = D act(G)   the same rows of Wu: the bn accumulator columns are
+//                                               G | U of bn/2 output columns, and one thread holds
+//                                               both values of an element
 //   GRADS      up to three products per launch: dW = dZ^T X (both operands MN-major, read from their
 //              row-major arrays) and dX = dZ W (+ dZ2 W2, the K loop running over both pairs)
 //
@@ -55,8 +56,7 @@
 namespace lce {
 namespace {
 
-constexpr int TILE = 256;               // rows and accumulator columns of a pair's tile
-constexpr int HALF = 128;               // B rows per CTA; output columns of a gated tile
+constexpr int TILE = 256;               // rows of a pair's tile, and its accumulator columns at most
 constexpr int BK = 64;                  // K elements per stage (one 128-byte swizzle span)
 constexpr int A_BYTES = BM * 128;
 constexpr int STAGE_BYTES = 2 * A_BYTES;
@@ -84,12 +84,6 @@ struct Cfg {
 constexpr int RASTER = 8;               // row tiles per rasterisation group (as in lce_tc.cu)
 constexpr int MAX_JOBS = 3;
 constexpr int MAX_SPLIT = 4;             // pairs that may sum one tile: clusters of 8 CTAs
-// Steps that the pieces of a K loop keep at least: of every product of a launch, or else of the long
-// ones only.
-template <bool F32>
-constexpr int MIN_STEPS = F32 ? 1 : 2;
-template <bool F32>
-constexpr int LONG_STEPS = F32 ? 2 : 6;
 constexpr int STATIC_WAVES = 4;         // tiles per pair up to which no scheduler counter is used
 constexpr int F32_STEP = 4;             // k-blocks per accumulator of an fp32 tile
 struct Ctl {
@@ -119,9 +113,9 @@ struct Job {
 struct KParams {
   Job job[MAX_JOBS];
   int njobs, total_tiles;
-  int planned[MAX_JOBS];   // host: the jobs' places in the plan
   int act;
   int split;               // pairs per cluster
+  int bn;                  // accumulator columns of a tile: 256 or 128
   const void* bias;
   int64_t m_rows;          // rows of Z
   // fp32 pre-activation gradients are written as parts, from registers
@@ -197,12 +191,13 @@ template <bool A_MN, bool B_MN, bool F32, int STAGES>
 __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, const CUtensorMap* mA,
                                              const CUtensorMap* mB, int m0, int n0, uint32_t base,
                                              Ctl* ctl, Ring& r, volatile int* abort_flag,
-                                             unsigned* err, uint32_t rank, uint32_t leader) {
+                                             unsigned* err, uint32_t rank, uint32_t leader,
+                                             int bn) {
   auto block = [&](const CUtensorMap* a, const CUtensorMap* b, int k0, int za, int zb) {
     const uint32_t full_local = ptx::smem_addr(&ctl->full[r.stage]);
     if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, err)) return false;
     const uint32_t full = ptx::mapa_shared(full_local, leader);
-    if (rank == 0) ptx::mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
+    if (rank == 0) ptx::mbar_arrive_expect_tx(full_local, 2 * A_BYTES + bn * 128);
     const uint32_t sa = base + r.stage * STAGE_BYTES, sb = sa + A_BYTES;
     if (A_MN) {
 #pragma unroll
@@ -212,9 +207,9 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, co
       ptx::tma_load_3d_pair(sa, a, k0, m0, za, full);
     }
     if (B_MN) {
-#pragma unroll
-      for (int c = 0; c < HALF / MN_BOX_ELEMS; ++c)
-        ptx::tma_load_3d_pair(sb + c * MN_BOX_BYTES, b, n0 + c * MN_BOX_ELEMS, k0, zb, full);
+      ptx::tma_load_3d_pair(sb, b, n0, k0, zb, full);
+      if (bn == TILE)
+        ptx::tma_load_3d_pair(sb + MN_BOX_BYTES, b, n0 + MN_BOX_ELEMS, k0, zb, full);
     } else {
       ptx::tma_load_3d_pair(sb, b, k0, n0, zb, full);
     }
@@ -242,8 +237,10 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, co
 
 template <bool A_MN, bool B_MN, int STAGES>
 __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t base, Ctl* ctl, Ring& r,
-                                         volatile int* abort_flag, unsigned* err, uint16_t pair_mask) {
-  constexpr uint32_t IDESC = ptx::idesc_bf16_f32(TILE, TILE, A_MN, B_MN);
+                                         volatile int* abort_flag, unsigned* err, uint16_t pair_mask,
+                                         int bn) {
+  const uint32_t idesc = bn == TILE ? ptx::idesc_bf16_f32(TILE, TILE, A_MN, B_MN)
+                                    : ptx::idesc_bf16_f32(TILE, TILE / 2, A_MN, B_MN);
   for (int kb = 0; kb < blocks; ++kb) {
     if (!wait_bar(ptx::smem_addr(&ctl->full[r.stage]), r.ph, abort_flag, err)) return false;
     ptx::tc_fence_after();
@@ -251,7 +248,7 @@ __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t b
 #pragma unroll
     for (int k = 0; k < BK / 16; ++k)
       ptx::tc_mma_f16_pair(d_tmem, A_MN ? desc_mnmajor(sa, k) : desc_kmajor(sa, k),
-                           B_MN ? desc_mnmajor(sb, k) : desc_kmajor(sb, k), IDESC, (kb | k) != 0);
+                           B_MN ? desc_mnmajor(sb, k) : desc_kmajor(sb, k), idesc, (kb | k) != 0);
     ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[r.stage]), pair_mask);
     if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
   }
@@ -265,10 +262,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// The four 32-column groups of accumulator columns that a warp of column half `half` drains.
+// The 32-column groups (4, or 2 where bn = 128) of accumulator columns that a warp of column half
+// `half` copies.
 template <bool GATED>
-__device__ __forceinline__ int half_col(int half, int h) {
-  return GATED ? (h >> 1) * HALF + half * (HALF / 2) + (h & 1) * 32 : half * HALF + h * 32;
+__device__ __forceinline__ int half_col(int half, int h, int bn) {
+  const int groups = bn / 64;
+  return GATED ? (h >= groups / 2) * (bn / 2) + half * (bn / 4) + (h & (groups / 2 - 1)) * 32
+               : half * (bn / 2) + h * 32;
 }
 
 // Element values of `E` per 16-byte chunk.
@@ -381,6 +381,20 @@ __device__ __forceinline__ void store_parts(const float (&v)[32], uint32_t stage
   __syncwarp();
 }
 
+// Tickets of one role: from the queue, or where no counters are used dealt out round-robin, which every
+// role of both CTAs works out for itself.
+struct Tickets {
+  TileQueue<true, Ctl> tq;
+  bool dealt;
+  int next, units, total;
+  __device__ __forceinline__ int take(unsigned mask) {
+    if (!dealt) return tq.take(mask);
+    const int t = next < total ? next : -1;
+    next += units;
+    return t;
+  }
+};
+
 template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     ffn_tc_kernel(const __grid_constant__ FMaps maps, const KParams p) {
@@ -449,8 +463,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int q = warp & 3;        // TMEM lane quadrant the warp may access
   const int half = e >> 2;       // which half of the columns it drains
   constexpr int UC = F32 ? 32 : 64;          // columns of one box
-  constexpr int COLS = GATED ? HALF : TILE;  // output columns of a tile
-  constexpr int UNITS = COLS / 2 / UC;       // boxes per warp and tile
+  const int cols = GATED ? p.bn / 2 : p.bn;  // output columns of a tile
+  const int nbox = cols / UC;                // its boxes: the first half of them (at least one) for
+  const int per_half = max(nbox / 2, 1);     // the warps of column half 0, the rest for half 1
+  const int groups = p.bn / 64;              // 32-column groups of accumulators per warp
   const uint32_t my_boxes = boxes + e * BOXES * STAGE_BUF_BYTES;
   const uint32_t sw = lane & 7;
   uint32_t box_ph = 0, in_flight = 0;  // a bit per box
@@ -510,8 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         ptx::bulk_commit();
       }
       if constexpr (MODE == FFN_GATED_DGU) {
-        // dU through the other box, which a bf16 tile loads nothing into
-        static_assert(F32 || UNITS == 1, "one box of D per warp and tile");
+        // dU through the other box: a bf16 tile has one box of D per warp
         const uint32_t row2 = my_boxes + (i ^ 1) * STAGE_BUF_BYTES + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -528,32 +543,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     return true;
   };
 
+  auto role_tickets = [&](bool remote) {
+    return Tickets{TileQueue<true, Ctl>{ctl, abort_flag, p.err, 0, 0u, remote, leader}, p.sched == nullptr,
+                   unit, units, p.total_tiles};
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
       bool ok = true;
       Ring ring{0, 0u};
-      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0, leader};
-      unsigned next = unit;
+      Tickets tickets = role_tickets(rank != 0);
+      TileQueue<true, Ctl>& tq = tickets.tq;
+      const bool posts = p.sched && rank == 0;  // this thread hands the tickets out
+      unsigned next = 0u;
       int upcoming = -1;
-      auto draw = [&] {  // the ticket after `next`
-        if (p.sched) next = atomicAdd(&p.sched[0], 1u);
-        else next += units;
-      };
-      if (rank == 0) {
-        if (p.sched) draw();
+      if (posts) {
+        next = atomicAdd(&p.sched[0], 1u);
         upcoming = tq.post(next, p.sched, p.total_tiles, units);
-        if (upcoming >= 0) draw();
+        if (upcoming >= 0) next = atomicAdd(&p.sched[0], 1u);
       }
       while (ok) {
         int tile;
-        if (rank == 0) {
+        if (posts) {
           tile = upcoming;
           if (tile < 0) break;
           upcoming = tq.post(next, p.sched, p.total_tiles, units);
-          if (upcoming >= 0) draw();
+          if (upcoming >= 0) next = atomicAdd(&p.sched[0], 1u);
         } else {
-          tile = tq.take(1u);
+          tile = tickets.take(1u);
         }
         if (tile < 0) break;
         const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
@@ -566,22 +584,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (GATED) {
           // CTA 0 loads its columns' rows of Wg, CTA 1 the same rows of Wu
           ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
-                                               tp.tn * HALF, base, ctl, ring, abort_flag, p.err,
-                                               rank, leader);
+                                               tp.tn * (p.bn / 2), base, ctl, ring, abort_flag, p.err,
+                                               rank, leader, p.bn);
         } else {
-          const int n0 = tp.tn * TILE + static_cast<int>(rank) * HALF;
+          const int n0 = tp.tn * p.bn + static_cast<int>(rank) * (p.bn / 2);
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
               ok = produce_tile<true, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                  maps.b[tp.job], m0, n0, base, ctl, ring, abort_flag,
-                                                 p.err, rank, leader);
+                                                 p.err, rank, leader, p.bn);
             else
               ok = produce_tile<false, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                   maps.b[tp.job], m0, n0, base, ctl, ring,
-                                                  abort_flag, p.err, rank, leader);
+                                                  abort_flag, p.err, rank, leader, p.bn);
           } else {
             ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
-                                                 ctl, ring, abort_flag, p.err, rank, leader);
+                                                 ctl, ring, abort_flag, p.err, rank, leader, p.bn);
           }
         }
       }
@@ -598,9 +616,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       Ring ring{0, 0u};
       int acc = 0;
       uint32_t aph = 0;
-      TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, false, leader};
+      Tickets tickets = role_tickets(false);
       while (ok) {
-        const int tile = tq.take(1u);
+        const int tile = tickets.take(1u);
         if (tile < 0) break;
         const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
         if (SPLIT && tp.tm < 0) continue;
@@ -621,11 +639,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t d_tmem = tmem_base + acc * TILE;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = mma_tile<true, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+              ok = mma_tile<true, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
             else
-              ok = mma_tile<false, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+              ok = mma_tile<false, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
           } else {
-            ok = mma_tile<false, false, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask);
+            ok = mma_tile<false, false, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
           }
           if (!ok) break;
           ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), pair_mask);
@@ -642,12 +660,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue (warps 2..9)
-    TileQueue<true, Ctl> tq{ctl, abort_flag, p.err, 0, 0u, rank != 0, leader};
+    Tickets tickets = role_tickets(rank != 0);
     int acc = 0;
     uint32_t aph = 0;
     bool ok = true;
     while (ok) {
-      const int tile = tq.take(0xffffffffu);
+      const int tile = tickets.take(0xffffffffu);
       if (tile < 0) break;
       const TilePos tp = SPLIT ? locate_split(p, tile, piece) : locate(p, tile);
       if (SPLIT && tp.tm < 0) continue;
@@ -657,15 +675,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Range range =
           piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, whole ? piece : 0, whole ? split : 1);
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
-      const int col0 = tp.tn * COLS + half * (COLS / 2);
+      const int col0 = tp.tn * cols + half * per_half * UC;
       // the n-th box of this warp: its first column.  Boxes of a tile that a cluster finishes together:
       // box b belongs to pair b % split, there to the warps of column half (b / split) % 2.
       auto box_col = [&](int n) {
-        return whole ? tp.tn * COLS + (piece + split * (half + 2 * n)) * UC : col0 + n * UC;
+        return whole ? tp.tn * cols + (piece + split * (half + 2 * n)) * UC : col0 + n * UC;
       };
-      const int col_end = min(jb.c_cols, (tp.tn + 1) * COLS);
+      // columns end with the result, the tile, or (direct) the half's boxes
+      const int col_end = min(min(jb.c_cols, (tp.tn + 1) * cols),
+                              whole ? jb.c_cols : col0 + per_half * UC);
       if (Cf::LOADS) {  // R or D of the first boxes, while the products run
-        for (int n = 0; n < min(BOXES, UNITS); ++n)
+        for (int n = 0; n < BOXES; ++n)
           if (box_col(n) < col_end) fetch(n, box_col(n), box_row);
       }
       // hand the accumulator back to the MMA issuer (in the pair's first CTA)
@@ -688,15 +708,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) { ok = false; break; }
           ptx::tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
-            ptx::tmem_add16(lanes + acc * TILE + half_col<GATED>(half, h >> 1) + (h & 1) * 16,
+          for (int h = 0; h < 8; ++h) {
+            if (h >= 2 * groups) break;
+            ptx::tmem_add16(lanes + acc * TILE + half_col<GATED>(half, h >> 1, p.bn) + (h & 1) * 16,
                             &sum[h >> 1][(h & 1) * 16]);
+          }
           if (st + 1 < steps) release();
         }
         if (!ok) break;
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          ptx::tmem_store32(lanes + acc * TILE + half_col<GATED>(half, h), sum[h]);
+          if (h < groups) ptx::tmem_store32(lanes + acc * TILE + half_col<GATED>(half, h, p.bn), sum[h]);
       } else if (!wait_bar(ptx::smem_addr(&ctl->tfull[acc]), aph, abort_flag, p.err)) {
         break;
       }
@@ -706,8 +728,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // This pair's partial sums into shared memory, four columns of a row together: every MMA is
         // done, so the ring is free.  The boxes follow below, once all pairs are here.
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const int c = half_col<GATED>(half, h);
+        for (int h = 0; h < groups; ++h) {
+          const int c = half_col<GATED>(half, h, p.bn);
           float v[32];
           ptx::tmem_load32(tbase + c, v);
 #pragma unroll
@@ -719,17 +741,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         split_tile = tile;
       } else {
 #pragma unroll 1
-        for (int un = 0; un < UNITS; ++un) {
+        for (int un = 0;; ++un) {
           const int col = col0 + un * UC;
           if (col >= col_end) break;  // same for every thread of the warp
-          const int at = half * (COLS / 2) + un * UC;  // accumulator column
+          const int at = (half * per_half + un) * UC;  // accumulator column
           ok = process(un % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
                        [&](int h, float (&z)[32], float (&u)[32]) {
                          ptx::tmem_load32(tbase + at + h * 32, z);
-                         if (GATED) ptx::tmem_load32(tbase + HALF + at + h * 32, u);
+                         if (GATED) ptx::tmem_load32(tbase + p.bn / 2 + at + h * 32, u);
                        });
           if (!ok) break;
-          if (Cf::LOADS && un + BOXES < UNITS && col + BOXES * UC < col_end)
+          if (Cf::LOADS && col + BOXES * UC < col_end)
             fetch(un % BOXES, col + BOXES * UC, box_row);
         }
         if (!ok) break;
@@ -746,7 +768,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Job& jb = p.job[tp.job];
       const int steps = steps_per_pair<F32>(jb.nkb) * jb.pairs;
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
-      const int col_end = min(jb.c_cols, (tp.tn + 1) * COLS);
+      const int col_end = min(jb.c_cols, (tp.tn + 1) * cols);
       // 32 columns from all pairs, in the order of the pieces
       auto gather = [&](int c, float (&v)[32]) {
         const uint32_t at = base + ((c >> 2) * BM + q * 32 + lane) * 16;
@@ -777,12 +799,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int n = 0;; ++n) {
         const int b = piece + split * (half + 2 * n);
-        const int col = tp.tn * COLS + b * UC;
+        const int col = tp.tn * cols + b * UC;
         if (col >= col_end) break;
         const bool ok = process(n % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
                                 [&](int h, float (&z)[32], float (&u)[32]) {
                                   gather(b * UC + h * 32, z);
-                                  if (GATED) gather(HALF + b * UC + h * 32, u);
+                                  if (GATED) gather(p.bn / 2 + b * UC + h * 32, u);
                                 });
         if (!ok) break;
         const int next = col + BOXES * 2 * split * UC;
@@ -838,29 +860,26 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, u
   return true;
 }
 
-// An operand [rows x K] (K-major), or stored [K x rows] (MN-major): 3-D, the parts last.
-bool operand(CUtensorMap* m, const FfnOperand& o, bool mn, const char* what) {
+// An operand [.. x K] (K-major, boxes of `rows` rows), or stored [K x ..] (MN-major): 3-D, the parts
+// last.
+bool operand(CUtensorMap* m, const FfnOperand& o, bool mn, int rows, const char* what) {
   const uint64_t ps = o.parts > 1 ? o.part_stride : static_cast<uint64_t>(o.ld) * o.stored_rows;
-  return make_map(m, o.ptr, o.stored_cols, o.stored_rows, o.ld, BK, mn ? BK : BM, false, 3, o.parts,
+  return make_map(m, o.ptr, o.stored_cols, o.stored_rows, o.ld, BK, mn ? BK : rows, false, 3, o.parts,
                   ps, what);
 }
 
-// What decides how a launch's sums are cut: all its products, asked for or not, so that a result is
-// the same bits whichever others are computed with it.
-struct Plan {
-  int n;
-  int tiles[MAX_JOBS], steps[MAX_JOBS];  // of each product; steps of its K loop
-};
-
-// Largest grid, in clusters of `pairs` CTA pairs, that the device holds at once (0: unknown).
-template <int MODE, bool F32>
+// Largest number of clusters of `pairs` CTA pairs that the device holds at once (every mode's kernel
+// takes the same room).
+template <bool F32>
 int max_clusters(int pairs) {
   static int cached[MAX_SPLIT + 1];
   if (cached[pairs] == 0) {
+    const auto kernel = ffn_tc_kernel<FFN_GRADS, F32, true>;
+    constexpr int bytes = Cfg<FFN_GRADS>::SMEM_BYTES;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cfg<MODE>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = bytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * pairs;
@@ -869,18 +888,84 @@ int max_clusters(int pairs) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, ffn_tc_kernel<MODE, F32, true>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       n = 0;
     }
     cached[pairs] = n > 0 ? n : -1;
   }
-  return cached[pairs] > 0 ? cached[pairs] : 0;
+  return std::max(cached[pairs], 0);
+}
+
+// How a launch's tiles and sums are cut.  It is chosen from all products of the launch, asked for or
+// not, so that a result is the same bits whichever others are computed with it.
+struct Plan {
+  int bn = TILE, split = 1;
+  bool whole[MAX_JOBS] = {};
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The cheapest of the tile widths and cluster sizes by an estimate in SM cycles, from measured parts: a
+// k-block costs 528 cycles in a 256 x 256 tile and about 390 in one of half the width (its operands
+// then bound it), finishing a 256 x 256 tile 3,000, and joining the pieces of one the transfer of its
+// partial sums at 14 bytes per cycle and SM (the rate distributed shared memory showed: 5 us for a
+// tile cut in four) after about 1,500 of synchronisation.
+template <bool F32>
+Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
+  Plan best;
+  double best_cost = 0.0;
+  for (int bn = TILE; bn >= TILE / 2; bn /= 2) {
+    const double step_cost = (bn == TILE ? 528.0 : 390.0) * (F32 ? 6 * F32_STEP : 1);
+    const double finish = 3000.0 * bn / TILE * (F32 ? 2 : 1);
+    int64_t tiles[MAX_JOBS], steps[MAX_JOBS], all = 0;
+    double work = 0.0, longest = 0.0;
+    for (int j = 0; j < njobs; ++j) {
+      const FfnTc& g = jobs[j];
+      tiles[j] = ceil_div(g.M, TILE) * ceil_div(g.Ncols, gated ? bn / 2 : bn);
+      steps[j] = steps_per_pair<F32>(static_cast<int>(ceil_div(g.K, BK))) * (!gated && g.A2.ptr ? 2 : 1);
+      all += tiles[j];
+      work += static_cast<double>(tiles[j]) * steps[j] * step_cost;
+      longest = std::max(longest, steps[j] * step_cost);
+    }
+    // pairs on their own: waves of one product's tiles; several products fill each other's gaps
+    double cost = all <= units ? longest
+                  : njobs == 1 ? ceil_div(all, units) * longest
+                               : work / units + longest / 2;
+    cost += finish;
+    if (best_cost == 0.0 || cost < best_cost) {
+      best_cost = cost;
+      best = Plan{};
+      best.bn = bn;
+    }
+    for (int k = 2; k <= MAX_SPLIT; k *= 2) {
+      // products are cut from `least` steps per piece on; the others' tiles lie side by side
+      for (const int least : {1, F32 ? 2 : 6}) {
+        int64_t clusters = 0;
+        double slowest = 0.0;
+        bool whole[MAX_JOBS] = {}, any = false;
+        for (int j = 0; j < njobs; ++j) {
+          whole[j] = steps[j] >= static_cast<int64_t>(least) * k;
+          any |= whole[j];
+          clusters += whole[j] ? tiles[j] : ceil_div(tiles[j], k);
+          const double join = 1500.0 + bn * BM * 4.0 * (k - 1) / k / 14.0;
+          slowest = std::max(slowest, whole[j] ? ceil_div(steps[j], k) * step_cost + join + finish / k
+                                               : steps[j] * step_cost + finish);
+        }
+        if (!any || clusters > max_clusters<F32>(k) || slowest >= best_cost) continue;
+        best_cost = slowest;
+        best.bn = bn;
+        best.split = k;
+        for (int j = 0; j < njobs; ++j) best.whole[j] = whole[j];
+      }
+    }
+  }
+  return best;
 }
 
 template <int MODE, bool F32>
-cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, bool dependent, int num_sms,
-                   cudaStream_t stream) {
+cudaError_t launch(const FMaps& maps, KParams& p, bool dependent, int num_sms, cudaStream_t stream) {
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
@@ -894,32 +979,9 @@ cudaError_t launch(const FMaps& maps, KParams& p, const Plan& plan, bool depende
     }
     attr_set = true;
   }
-  // Few tiles: each is summed by 2 or 4 pairs, as long as all clusters run at once.  Where that does
-  // not fit for every product of the launch, only those with a long K loop are cut and the pairs of a
-  // cluster take tiles of the others side by side.
-  p.split = 1;
-  bool whole[MAX_JOBS] = {};
-  for (int k = 2; k <= MAX_SPLIT; k *= 2) {
-    for (int least = MIN_STEPS<F32>; least <= LONG_STEPS<F32>; least = least < LONG_STEPS<F32> ? LONG_STEPS<F32> : least + 1) {
-      int64_t clusters = 0;
-      bool any = false;
-      for (int j = 0; j < plan.n; ++j) {
-        const bool w = plan.steps[j] >= least * k;
-        any |= w;
-        clusters += w ? plan.tiles[j] : (plan.tiles[j] + k - 1) / k;
-      }
-      if (!any || clusters > max_clusters<MODE, F32>(k)) continue;
-      p.split = k;
-      for (int j = 0; j < plan.n; ++j) whole[j] = plan.steps[j] >= least * k;
-      break;
-    }
-  }
   int clusters = 0;
-  for (int j = 0; j < p.njobs; ++j) {
-    Job& jb = p.job[j];
-    jb.whole = p.split > 1 && whole[p.planned[j]];
-    clusters += jb.whole ? jb.num_tiles : (jb.num_tiles + p.split - 1) / p.split;
-  }
+  for (int j = 0; j < p.njobs; ++j)
+    clusters += static_cast<int>(p.job[j].whole ? p.job[j].num_tiles : ceil_div(p.job[j].num_tiles, p.split));
   const int units = num_sms / 2;
   cudaLaunchConfig_t cfg = {};
   if (p.split > 1) p.total_tiles = clusters;  // a ticket is a cluster's work
@@ -954,16 +1016,18 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   const bool gated = mode == FFN_GATED || mode == FFN_GATED_DGU;
   const bool dz = mode == FFN_LINEAR_DZ || mode == FFN_GATED_DGU;
   const uint32_t uc = F32 ? 32 : 64;
-  Plan plan{};
-  int64_t all_tiles = 0;
+  for (int i = 0; i < njobs; ++i)
+    if (ceil_div(jobs[i].K, BK) > (1 << 25)) return cudaErrorInvalidValue;  // widths end at 2^31
+  const Plan plan = choose_plan<F32>(jobs, njobs, gated, num_sms / 2);
+  p.split = plan.split;
+  p.bn = plan.bn;
   int n = 0;
   for (int i = 0; i < njobs; ++i) {
     const FfnTc& g = jobs[i];
     Job jb{};
-    const int64_t cols = gated ? HALF : TILE;
-    const int64_t tm = (g.M + TILE - 1) / TILE, tn = (g.Ncols + cols - 1) / cols;
-    const int64_t nkb = (g.K + BK - 1) / BK;
-    if (tm * tn > (int64_t(1) << 28) || all_tiles + tm * tn > (int64_t(1) << 29) || nkb > (1 << 25)) {
+    if (!g.C) continue;  // a result that is not asked for counts in the plan only
+    const int64_t tm = ceil_div(g.M, TILE), tn = ceil_div(g.Ncols, gated ? p.bn / 2 : p.bn);
+    if (tm * tn > (int64_t(1) << 28)) {
       set_error_detail("feed-forward product of %lld x %lld tiles: beyond the scheduler's range",
                        static_cast<long long>(tm), static_cast<long long>(tn));
       return cudaErrorInvalidValue;
@@ -971,23 +1035,19 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
     jb.tiles_m = static_cast<int>(tm);
     jb.tiles_n = static_cast<int>(tn);
     jb.num_tiles = jb.tiles_m * jb.tiles_n;
-    jb.nkb = static_cast<int>(nkb);
+    jb.nkb = static_cast<int>(ceil_div(g.K, BK));
     jb.pairs = (!gated && g.A2.ptr) ? 2 : 1;
     jb.mn = g.a_mn;
     jb.c_cols = static_cast<int>(g.Ncols);
-    all_tiles += jb.num_tiles;
-    plan.tiles[plan.n] = jb.num_tiles;
-    plan.steps[plan.n++] = steps_per_pair<F32>(jb.nkb) * jb.pairs;
-    if (!g.C) continue;  // a result that is not asked for counts in the plan only
+    jb.whole = plan.split > 1 && plan.whole[i];
     const int j = n++;
     p.job[j] = jb;
-    p.planned[j] = plan.n - 1;
     p.total_tiles += jb.num_tiles;
-    if (!operand(&maps.a[j][0], g.A, g.a_mn, "A") || !operand(&maps.b[j][0], g.B, g.b_mn, "B"))
-      return cudaErrorInvalidResourceHandle;
-    if (gated && !operand(&maps.b[j][1], g.B2, g.b_mn, "B2")) return cudaErrorInvalidResourceHandle;
-    if (jb.pairs == 2 && (!operand(&maps.a[j][1], g.A2, g.a_mn, "A2") ||
-                          !operand(&maps.b[j][1], g.B2, g.b_mn, "B2")))
+    const int b_rows = p.bn / 2;
+    if (!operand(&maps.a[j][0], g.A, g.a_mn, BM, "A") ||
+        !operand(&maps.b[j][0], g.B, g.b_mn, b_rows, "B") ||
+        (jb.pairs == 2 && !operand(&maps.a[j][1], g.A2, g.a_mn, BM, "A2")) ||
+        ((gated || jb.pairs == 2) && !operand(&maps.b[j][1], g.B2, g.b_mn, b_rows, "B2")))
       return cudaErrorInvalidResourceHandle;
     if (!(dz && F32)) {
       if (!make_map(&maps.c[j], g.C, g.Ncols, g.M, g.ldc, uc, 32, F32, 2, 1, 0, "C"))
@@ -1033,12 +1093,12 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   state->flags = true;
   switch (mode) {
     case FFN_LINEAR:
-      return d ? launch<FFN_LINEAR_RES, F32>(maps, p, plan, dependent, num_sms, stream)
-               : launch<FFN_LINEAR, F32>(maps, p, plan, dependent, num_sms, stream);
-    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, plan, dependent, num_sms, stream);
-    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, plan, dependent, num_sms, stream);
-    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, plan, dependent, num_sms, stream);
-    default: return launch<FFN_GRADS, F32>(maps, p, plan, dependent, num_sms, stream);
+      return d ? launch<FFN_LINEAR_RES, F32>(maps, p, dependent, num_sms, stream)
+               : launch<FFN_LINEAR, F32>(maps, p, dependent, num_sms, stream);
+    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, dependent, num_sms, stream);
+    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, dependent, num_sms, stream);
+    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, dependent, num_sms, stream);
+    default: return launch<FFN_GRADS, F32>(maps, p, dependent, num_sms, stream);
   }
 }
 

@@ -11,34 +11,36 @@
 #include <math.h>
 
 #include "lce.h"
+#include "ptx.cuh"
 
 namespace lce {
 
-template <bool FAST>
-__device__ __forceinline__ float sigmoid(float x) {
-  // x below about -87: e^-x passes 2^126 and the quotient, approximate or not, is 0
-  if (FAST) return __fdividef(1.f, 1.f + __expf(-x));
-  return 1.f / (1.f + expf(-x));
-}
-
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x) {
+  // x below about -88: e^-x is huge or inf and the quotient 0
+  if (FAST) return ptx::rcp_approx(1.f + ptx::ex2_approx(-kLog2e * x));
+  return 1.f / (1.f + expf(-x));
+}
 
 // Phi(x) and e = exp(-x^2 / 2), for bf16 results.  The upper tail Q(y) = erfc(y / sqrt 2) / 2 is
 // e t P(t) / 2 with t = 1 / (1 + 0.46 y / sqrt 2); the degree-5 P was fitted to exp(z^2) erfc(z) / t on
 // z >= 0 (least squares in t, reweighted towards the largest relative error, 1.8e-5).  One exponential
 // and one quotient serve Phi and the density in its derivative.
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
-  const float t = __fdividef(1.f, fmaf(0.46f * kSqrtHalf, fabsf(x), 1.f));
-  e = __expf(-0.5f * x * x);
-  float p = -0.12635274f;
-  p = fmaf(p, t, 0.24180298f);
-  p = fmaf(p, t, 0.12544967f);
-  p = fmaf(p, t, 0.24052443f);
-  p = fmaf(p, t, 0.25903428f);
-  p = fmaf(p, t, 0.25953171f);
-  const float q = 0.5f * e * (t * p);
+  const float t = ptx::rcp_approx(fmaf(0.46f * kSqrtHalf, fabsf(x), 1.f));
+  e = ptx::ex2_approx(-0.5f * kLog2e * x * x);
+  float p = 0.5f * -0.12635274f;  // P / 2
+  p = fmaf(p, t, 0.5f * 0.24180298f);
+  p = fmaf(p, t, 0.5f * 0.12544967f);
+  p = fmaf(p, t, 0.5f * 0.24052443f);
+  p = fmaf(p, t, 0.5f * 0.25903428f);
+  p = fmaf(p, t, 0.5f * 0.25953171f);
+  const float q = e * (t * p);
   return x > 0.f ? 1.f - q : q;
 }
 

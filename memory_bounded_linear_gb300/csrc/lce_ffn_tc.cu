@@ -34,8 +34,8 @@
 // The outgoing gradient D and the residual R enter, and C leaves, through 4 KB boxes of the epilogue
 // warps (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
 // store.  Modes that load boxes have two per warp, both fetched while the products of their tile
-// run, and a ring of five 32 KB stages; the others one box and six stages (with one box the epilogue
-// of 4095 x 2048 -> 8192 took twice the products' time: it waited for each box in turn).
+// run, and a ring of five 32 KB stages; so have the others while K is short, where the epilogue decides
+// (a warp then fills one box while the other leaves); with long K they have one box and six stages.
 //
 // Bound: tensor pipe for many tokens.  Ragged edges: TMA zero-fills loads and clips stores.
 #include <cuda.h>
@@ -73,18 +73,25 @@ struct Cfg {
   static constexpr bool GATED = MODE == FFN_GATED || MODE == FFN_GATED_DGU;
   static constexpr bool DZ = MODE == FFN_LINEAR_DZ || MODE == FFN_GATED_DGU;
   static constexpr bool LOADS = DZ || MODE == FFN_LINEAR_RES;  // boxes of D or R are loaded
-  static constexpr int BOXES = LOADS ? 2 : 1;                  // per epilogue warp
-  static constexpr int STAGES = LOADS ? 5 : 6;
-  static constexpr int BOX_BYTES = EPI_WARPS * BOXES * STAGE_BUF_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BOX_BYTES + 1024 + CTL_BYTES;
-  static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
-  // a tile's partial sums (SPLIT) fit in the ring
-  static_assert(STAGES * STAGE_BYTES >= TILE * BM * 4, "ring smaller than an accumulator");
 };
+
+// Shared memory: the stages of the ring, then the boxes of the eight epilogue warps: six stages and one
+// box per warp, or five and two.
+constexpr int RING_AND_BOXES = 6 * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES;
+constexpr int SMEM_BYTES = RING_AND_BOXES + 1024 + CTL_BYTES;
+static_assert(5 * STAGE_BYTES + 2 * EPI_WARPS * STAGE_BUF_BYTES == RING_AND_BOXES, "one size");
+static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory per CTA");
+// a tile's partial sums (SPLIT) fit in the ring
+static_assert(5 * STAGE_BYTES >= TILE * BM * 4, "ring smaller than an accumulator");
+// K-blocks of a tile up to which two boxes are worth a stage.
+constexpr int SHORT_K = 12;
 constexpr int RASTER = 8;               // row tiles per rasterisation group (as in lce_tc.cu)
 constexpr int MAX_JOBS = 3;
 constexpr int MAX_SPLIT = 4;             // pairs that may sum one tile: clusters of 8 CTAs
-constexpr int STATIC_WAVES = 4;         // tiles per pair up to which no scheduler counter is used
+// Tiles per pair up to which they are dealt out without a scheduler counter: in launches of one
+// product, and of several, whose tiles take different times.
+constexpr int DEALT_WAVES = 20;
+constexpr int DEALT_WAVES_MIXED = 2;
 constexpr int F32_STEP = 4;             // k-blocks per accumulator of an fp32 tile
 struct Ctl {
   uint64_t full[MAX_STAGES];
@@ -116,6 +123,7 @@ struct KParams {
   int act;
   int split;               // pairs per cluster
   int bn;                  // accumulator columns of a tile: 256 or 128
+  int boxes;               // per epilogue warp, modes that load none: 1 or 2
   const void* bias;
   int64_t m_rows;          // rows of Z
   // fp32 pre-activation gradients are written as parts, from registers
@@ -187,12 +195,12 @@ __device__ __forceinline__ TilePos locate_split(const KParams& p, int unit, int 
 }
 
 // Producer side of one tile.  A_MN, B_MN: the operand is MN-major.
-template <bool A_MN, bool B_MN, bool F32, int STAGES>
+template <bool A_MN, bool B_MN, bool F32>
 __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, const CUtensorMap* mA,
                                              const CUtensorMap* mB, int m0, int n0, uint32_t base,
                                              Ctl* ctl, Ring& r, volatile int* abort_flag,
                                              unsigned* err, uint32_t rank, uint32_t leader,
-                                             int bn) {
+                                             int bn, int stages) {
   auto block = [&](const CUtensorMap* a, const CUtensorMap* b, int k0, int za, int zb) {
     const uint32_t full_local = ptx::smem_addr(&ctl->full[r.stage]);
     if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, err)) return false;
@@ -213,7 +221,7 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, co
     } else {
       ptx::tma_load_3d_pair(sb, b, k0, n0, zb, full);
     }
-    if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
+    if (++r.stage == stages) { r.stage = 0; r.ph ^= 1u; }
     return true;
   };
   const int per_pair = steps_per_pair<F32>(nkb);
@@ -235,10 +243,10 @@ __device__ __forceinline__ bool produce_tile(int nkb, int pairs, Range range, co
   return true;
 }
 
-template <bool A_MN, bool B_MN, int STAGES>
+template <bool A_MN, bool B_MN>
 __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t base, Ctl* ctl, Ring& r,
                                          volatile int* abort_flag, unsigned* err, uint16_t pair_mask,
-                                         int bn) {
+                                         int bn, int stages) {
   const uint32_t idesc = bn == TILE ? ptx::idesc_bf16_f32(TILE, TILE, A_MN, B_MN)
                                     : ptx::idesc_bf16_f32(TILE, TILE / 2, A_MN, B_MN);
   for (int kb = 0; kb < blocks; ++kb) {
@@ -250,7 +258,7 @@ __device__ __forceinline__ bool mma_tile(int blocks, uint32_t d_tmem, uint32_t b
       ptx::tc_mma_f16_pair(d_tmem, A_MN ? desc_mnmajor(sa, k) : desc_kmajor(sa, k),
                            B_MN ? desc_mnmajor(sb, k) : desc_kmajor(sb, k), idesc, (kb | k) != 0);
     ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[r.stage]), pair_mask);
-    if (++r.stage == STAGES) { r.stage = 0; r.ph ^= 1u; }
+    if (++r.stage == stages) { r.stage = 0; r.ph ^= 1u; }
   }
   return true;
 }
@@ -400,13 +408,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     ffn_tc_kernel(const __grid_constant__ FMaps maps, const KParams p) {
   using Cf = Cfg<MODE>;
   constexpr bool GATED = Cf::GATED, DZ = Cf::DZ;
-  constexpr int STAGES = Cf::STAGES, BOXES = Cf::BOXES;
+  const int nboxes = Cf::LOADS ? 2 : p.boxes;  // per epilogue warp
+  const int stages = 7 - nboxes;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;  // 128B-swizzled tiles need 1024B alignment
   uint8_t* smem = smem_raw + (base - raw_addr);
-  const uint32_t boxes = base + STAGES * STAGE_BYTES;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES + Cf::BOX_BYTES);
+  const uint32_t boxes = base + stages * STAGE_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + RING_AND_BOXES);
   volatile int* abort_flag = &ctl->abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int unit = static_cast<int>(blockIdx.x >> 1) / split;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
     }
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // readers: MMA issuer, the second CTA's producer, the epilogue warps of both
       ptx::mbar_init(ptx::smem_addr(&ctl->tq_empty[i]), 2 + 2 * EPI_WARPS);
     }
-    for (int i = 0; i < EPI_WARPS * BOXES; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->box[i]), 1);
+    for (int i = 0; i < EPI_WARPS * nboxes; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->box[i]), 1);
     ctl->abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -467,11 +476,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int nbox = cols / UC;                // its boxes: the first half of them (at least one) for
   const int per_half = max(nbox / 2, 1);     // the warps of column half 0, the rest for half 1
   const int groups = p.bn / 64;              // 32-column groups of accumulators per warp
-  const uint32_t my_boxes = boxes + e * BOXES * STAGE_BUF_BYTES;
+  const uint32_t my_boxes = boxes + e * nboxes * STAGE_BUF_BYTES;
   const uint32_t sw = lane & 7;
   uint32_t box_ph = 0, in_flight = 0;  // a bit per box
   int split_tile = -1;                 // SPLIT: the cluster whose tile is finished together
-  auto box_bar = [&](int i) { return ptx::smem_addr(&ctl->box[e * BOXES + i]); };
+  auto box_bar = [&](int i) { return ptx::smem_addr(&ctl->box[e * nboxes + i]); };
   // R or D of one box of results into box i, once the stores from the boxes have been read
   auto fetch = [&](int i, int col, int box_row) {
     if (lane == 0) {
@@ -482,15 +491,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     in_flight |= 1u << i;
   };
   // One box of results through box i: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32
-  // accumulator columns of the thread's row.  False when a wait gave up.
-  auto process = [&](int i, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load) {
+  // accumulator columns of the thread's row; loaded() is called once all have been read.  False when a
+  // wait gave up.
+  auto process = [&](int i, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load,
+                     auto&& loaded) {
     const uint32_t box = my_boxes + i * STAGE_BUF_BYTES, row_addr = box + lane * 128;
     if (Cf::LOADS) {
       if (!wait_bar(box_bar(i), (box_ph >> i) & 1u, abort_flag, p.err)) return false;
       in_flight &= ~(1u << i);
       box_ph ^= 1u << i;
     } else {
-      if (lane == 0) ptx::bulk_wait_read<0>();
+      if (lane == 0) {  // the box's last store has been read
+        if (nboxes == 2) ptx::bulk_wait_read<1>();
+        else ptx::bulk_wait_read<0>();
+      }
       __syncwarp();
     }
     [[maybe_unused]] uint32_t keep[MODE == FFN_GATED_DGU && !F32 ? 32 : 1];
@@ -498,6 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int h = 0; h < UC / 32; ++h) {
       float z[32], u[32];
       load(h, z, u);
+      if (h == UC / 32 - 1) loaded();
       if constexpr (MODE == FFN_GRADS)
         epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols, nullptr);
       else
@@ -583,23 +598,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             piece_of(steps_per_pair<F32>(jb.nkb) * jb.pairs, whole ? piece : 0, whole ? split : 1);
         if constexpr (GATED) {
           // CTA 0 loads its columns' rows of Wg, CTA 1 the same rows of Wu
-          ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
+          ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
                                                tp.tn * (p.bn / 2), base, ctl, ring, abort_flag, p.err,
-                                               rank, leader, p.bn);
+                                               rank, leader, p.bn,
+                                                 stages);
         } else {
           const int n0 = tp.tn * p.bn + static_cast<int>(rank) * (p.bn / 2);
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = produce_tile<true, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+              ok = produce_tile<true, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                  maps.b[tp.job], m0, n0, base, ctl, ring, abort_flag,
-                                                 p.err, rank, leader, p.bn);
+                                                 p.err, rank, leader, p.bn,
+                                                 stages);
             else
-              ok = produce_tile<false, true, F32, STAGES>(jb.nkb, jb.pairs, range, maps.a[tp.job],
+              ok = produce_tile<false, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                   maps.b[tp.job], m0, n0, base, ctl, ring,
-                                                  abort_flag, p.err, rank, leader, p.bn);
+                                                  abort_flag, p.err, rank, leader, p.bn,
+                                                 stages);
           } else {
-            ok = produce_tile<false, false, F32, STAGES>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
-                                                 ctl, ring, abort_flag, p.err, rank, leader, p.bn);
+            ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
+                                                 ctl, ring, abort_flag, p.err, rank, leader, p.bn,
+                                                 stages);
           }
         }
       }
@@ -639,11 +658,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t d_tmem = tmem_base + acc * TILE;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = mma_tile<true, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
+              ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
+                                       stages);
             else
-              ok = mma_tile<false, true, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
+              ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
+                                       stages);
           } else {
-            ok = mma_tile<false, false, STAGES>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn);
+            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
+                                       stages);
           }
           if (!ok) break;
           ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), pair_mask);
@@ -685,15 +707,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int col_end = min(min(jb.c_cols, (tp.tn + 1) * cols),
                               whole ? jb.c_cols : col0 + per_half * UC);
       if (Cf::LOADS) {  // R or D of the first boxes, while the products run
-        for (int n = 0; n < BOXES; ++n)
+        for (int n = 0; n < nboxes; ++n)
           if (box_col(n) < col_end) fetch(n, box_col(n), box_row);
       }
       // hand the accumulator back to the MMA issuer (in the pair's first CTA)
       auto release = [&]() {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0)
-          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->tempty[acc]), leader));
+        if (lane == 0) {  // nothing but the tensor memory is handed over
+          const uint32_t empty = ptx::smem_addr(&ctl->tempty[acc]);
+          if (rank == 0) ptx::mbar_arrive(empty);
+          else ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(empty, leader));
+        }
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
       };
@@ -739,24 +764,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                               __float_as_uint(v[i + 3]));
         }
         split_tile = tile;
+        release();
       } else {
+        if (col0 >= col_end) release();  // no box for this warp
 #pragma unroll 1
         for (int un = 0;; ++un) {
           const int col = col0 + un * UC;
           if (col >= col_end) break;  // same for every thread of the warp
           const int at = (half * per_half + un) * UC;  // accumulator column
-          ok = process(un % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
+          ok = process(un & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
                        [&](int h, float (&z)[32], float (&u)[32]) {
                          ptx::tmem_load32(tbase + at + h * 32, z);
                          if (GATED) ptx::tmem_load32(tbase + p.bn / 2 + at + h * 32, u);
-                       });
+                       },
+                       [&] { if (col + UC >= col_end) release(); });
           if (!ok) break;
-          if (Cf::LOADS && col + BOXES * UC < col_end)
-            fetch(un % BOXES, col + BOXES * UC, box_row);
+          if (Cf::LOADS && col + nboxes * UC < col_end)
+            fetch(un & (nboxes - 1), col + nboxes * UC, box_row);
         }
         if (!ok) break;
       }
-      release();
     }
   }
 
@@ -801,19 +828,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int b = piece + split * (half + 2 * n);
         const int col = tp.tn * cols + b * UC;
         if (col >= col_end) break;
-        const bool ok = process(n % BOXES, &maps.c[tp.job], jb.c_cols, col, box_row,
+        const bool ok = process(n & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
                                 [&](int h, float (&z)[32], float (&u)[32]) {
                                   gather(b * UC + h * 32, z);
                                   if (GATED) gather(p.bn / 2 + b * UC + h * 32, u);
-                                });
+                                },
+                                [] {});
         if (!ok) break;
-        const int next = col + BOXES * 2 * split * UC;
-        if (Cf::LOADS && next < col_end) fetch(n % BOXES, next, box_row);
+        const int next = col + nboxes * 2 * split * UC;
+        if (Cf::LOADS && next < col_end) fetch(n & (nboxes - 1), next, box_row);
       }
     }
   }
   if (warp >= 2) {
-    for (int i = 0; i < BOXES; ++i)
+    for (int i = 0; i < nboxes; ++i)
       if ((in_flight >> i) & 1u) wait_bar_drain(box_bar(i), (box_ph >> i) & 1u, 100000000ull);
     if (lane == 0) ptx::bulk_wait<0>();  // this warp's output stores have landed
     __syncwarp();
@@ -875,7 +903,7 @@ int max_clusters(int pairs) {
   static int cached[MAX_SPLIT + 1];
   if (cached[pairs] == 0) {
     const auto kernel = ffn_tc_kernel<FFN_GRADS, F32, true>;
-    constexpr int bytes = Cfg<FFN_GRADS>::SMEM_BYTES;
+    constexpr int bytes = SMEM_BYTES;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
@@ -969,10 +997,10 @@ cudaError_t launch(const FMaps& maps, KParams& p, bool dependent, int num_sms, c
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MODE>::SMEM_BYTES);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MODE>::SMEM_BYTES);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) {
       set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(e));
       return e;
@@ -987,7 +1015,7 @@ cudaError_t launch(const FMaps& maps, KParams& p, bool dependent, int num_sms, c
   if (p.split > 1) p.total_tiles = clusters;  // a ticket is a cluster's work
   cfg.gridDim = dim3(2 * (p.split > 1 ? clusters * p.split : std::min(p.total_tiles, units)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<MODE>::SMEM_BYTES;
+  cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1021,6 +1049,9 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   const Plan plan = choose_plan<F32>(jobs, njobs, gated, num_sms / 2);
   p.split = plan.split;
   p.bn = plan.bn;
+  int64_t longest = 0;
+  for (int i = 0; i < njobs; ++i) longest = std::max(longest, ceil_div(jobs[i].K, BK) * (jobs[i].A2.ptr ? 2 : 1));
+  p.boxes = !F32 && longest <= SHORT_K ? 2 : 1;
   int n = 0;
   for (int i = 0; i < njobs; ++i) {
     const FfnTc& g = jobs[i];
@@ -1073,10 +1104,12 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
     p.part_stride = g.part_stride;
   }
   p.err = header;
-  // A few waves of tiles are dealt out round-robin, which needs nothing cleared beforehand; longer
-  // launches take tickets from the counters in the header, which keeps tiles that share operands
-  // together however unevenly the SMs progress.
-  if (p.total_tiles > STATIC_WAVES * (num_sms / 2)) {
+  // Tiles are dealt out round-robin, or taken as tickets from the counters in the header.  Dealing needs
+  // nothing cleared beforehand and no hand-over between the roles (4096 x 512 x 8192: 32 us, 40 with
+  // tickets; x 2048: 77, 85); tickets even out tiles of different lengths (backward products of 512 x
+  // 4096 x 8192: 58 us, 67 dealt) and keep tiles that share operands together over long launches
+  // (gated backward 16384 x 4096 x 16384: 7.06 ms, 7.25 dealt).
+  if (p.total_tiles > (njobs == 1 ? DEALT_WAVES : DEALT_WAVES_MIXED) * (num_sms / 2)) {
     p.sched = header + WS_SCHED_WORD;
     const size_t from = state->flags ? WS_SCHED_WORD * sizeof(unsigned) : 0;
     if (!state->sched) {

@@ -20,6 +20,19 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// ---------------------------------------------------------------------------- approximate functions
+// 2^x and 1/x by the special function unit: relative error about 2^-22, subnormal results are 0.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------------------- dependent launches
 // Lets the next launch on the stream, if it was made as a dependent one, start its CTAs once every
 // CTA of this grid has come here.
@@ -308,6 +321,12 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, int v) 
 // Arrive on an mbarrier given by its cluster-window address (possibly in the peer CTA).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// The same without ordering this thread's earlier memory accesses: for hand-overs that pass no data
+// through memory (the release would wait for the thread's stores in flight).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 // 2-D tiled load into this CTA's shared memory whose completion is counted on an mbarrier that

@@ -32,8 +32,9 @@
 // them, read through distributed shared memory in the order of the pieces.
 //
 // The outgoing gradient D and the residual R enter, and C leaves, through 4 KB boxes of the epilogue
-// warps (32 rows x 128 bytes, 128-byte swizzle): TMA load, each thread rewrites its own row, TMA
-// store.  Modes that load boxes have two per warp, both fetched while the products of their tile
+// warps (32 rows x 128 bytes, 128-byte swizzle): 16-byte copies by the warp's lanes, each thread rewrites
+// its own row, TMA store.  (Boxes loaded by TMA held up the operands behind them in its queue: tiles
+// of 4096 x 2048 -> 8192 took 22,000 cycles instead of 17,000.)  Modes that load boxes have two per warp, both fetched while the products of their tile
 // run, and a ring of five 32 KB stages; so have the others while K is short, where the epilogue decides
 // (a warp then fills one box while the other leaves); with long K they have one box and six stages.
 //
@@ -65,7 +66,6 @@ constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 2 * TILE;
 constexpr int CTL_BYTES = 512;
 constexpr int MAX_STAGES = 6;
-constexpr int MAX_BOXES = 2;
 constexpr int FFN_LINEAR_RES = 5;       // FFN_LINEAR with a residual, a kernel of its own
 
 template <int MODE>
@@ -101,7 +101,6 @@ struct Ctl {
   uint64_t drain;
   uint64_t tq_full[TQ];
   uint64_t tq_empty[TQ];
-  uint64_t box[EPI_WARPS * MAX_BOXES];
   int tq[TQ];
   uint32_t tmem_base;
   int abort_flag;
@@ -125,6 +124,8 @@ struct KParams {
   int bn;                  // accumulator columns of a tile: 256 or 128
   int boxes;               // per epilogue warp, modes that load none: 1 or 2
   const void* bias;
+  const char* d;           // R or D, row stride in bytes
+  int64_t d_stride;
   int64_t m_rows;          // rows of Z
   // fp32 pre-activation gradients are written as parts, from registers
   __nv_bfloat16* parts[2];
@@ -139,7 +140,6 @@ struct FMaps {
   CUtensorMap b[MAX_JOBS][2];
   CUtensorMap c[MAX_JOBS];
   CUtensorMap c2;
-  CUtensorMap d;
 };
 
 // The six part products, smallest first: operand parts of A and B.
@@ -444,7 +444,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       // readers: MMA issuer, the second CTA's producer, the epilogue warps of both
       ptx::mbar_init(ptx::smem_addr(&ctl->tq_empty[i]), 2 + 2 * EPI_WARPS);
     }
-    for (int i = 0; i < EPI_WARPS * nboxes; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->box[i]), 1);
     ctl->abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -478,28 +477,37 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int groups = p.bn / 64;              // 32-column groups of accumulators per warp
   const uint32_t my_boxes = boxes + e * nboxes * STAGE_BUF_BYTES;
   const uint32_t sw = lane & 7;
-  uint32_t box_ph = 0, in_flight = 0;  // a bit per box
+  uint32_t in_flight = 0;              // boxes being loaded, a bit each
   int split_tile = -1;                 // SPLIT: the cluster whose tile is finished together
-  auto box_bar = [&](int i) { return ptx::smem_addr(&ctl->box[e * nboxes + i]); };
-  // R or D of one box of results into box i, once the stores from the boxes have been read
-  auto fetch = [&](int i, int col, int box_row) {
-    if (lane == 0) {
-      ptx::bulk_wait_read<0>();
-      ptx::mbar_arrive_expect_tx(box_bar(i), STAGE_BUF_BYTES);
-      ptx::tma_load_2d(my_boxes + i * STAGE_BUF_BYTES, &maps.d, col, box_row, box_bar(i));
+  // R or D of one box of results into box i, once the stores from the boxes have been read: eight lanes
+  // copy a row's 128 bytes; zeros outside the result.
+  auto fetch = [&](int i, int c_cols, int col, int box_row) {
+    if (lane == 0) ptx::bulk_wait_read<0>();
+    __syncwarp();
+    const int c = lane & 7;
+    const bool col_ok = col + c * CHUNK<F32> < c_cols;
+    const int64_t at = static_cast<int64_t>(col) * (F32 ? 4 : 2) + c * 16;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = k * 4 + (lane >> 3);
+      const bool ok = col_ok && box_row + r < p.m_rows;
+      ptx::copy16_async(my_boxes + i * STAGE_BUF_BYTES + r * 128 + ((c ^ (r & 7)) << 4),
+                        p.d + (ok ? (box_row + r) * p.d_stride + at : 0), ok);
     }
+    ptx::copy_commit();
     in_flight |= 1u << i;
   };
   // One box of results through box i: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32
-  // accumulator columns of the thread's row; loaded() is called once all have been read.  False when a
-  // wait gave up.
+  // accumulator columns of the thread's row; loaded() is called once all have been read.
   auto process = [&](int i, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load,
                      auto&& loaded) {
     const uint32_t box = my_boxes + i * STAGE_BUF_BYTES, row_addr = box + lane * 128;
     if (Cf::LOADS) {
-      if (!wait_bar(box_bar(i), (box_ph >> i) & 1u, abort_flag, p.err)) return false;
+      // the other box, if it is being loaded, was asked for later
       in_flight &= ~(1u << i);
-      box_ph ^= 1u << i;
+      if (in_flight) ptx::copy_wait<1>();
+      else ptx::copy_wait<0>();
+      __syncwarp();
     } else {
       if (lane == 0) {  // the box's last store has been read
         if (nboxes == 2) ptx::bulk_wait_read<1>();
@@ -555,7 +563,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    return true;
   };
 
   auto role_tickets = [&](bool remote) {
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                               whole ? jb.c_cols : col0 + per_half * UC);
       if (Cf::LOADS) {  // R or D of the first boxes, while the products run
         for (int n = 0; n < nboxes; ++n)
-          if (box_col(n) < col_end) fetch(n, box_col(n), box_row);
+          if (box_col(n) < col_end) fetch(n, jb.c_cols, box_col(n), box_row);
       }
       // hand the accumulator back to the MMA issuer (in the pair's first CTA)
       auto release = [&]() {
@@ -772,17 +779,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int col = col0 + un * UC;
           if (col >= col_end) break;  // same for every thread of the warp
           const int at = (half * per_half + un) * UC;  // accumulator column
-          ok = process(un & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
-                       [&](int h, float (&z)[32], float (&u)[32]) {
-                         ptx::tmem_load32(tbase + at + h * 32, z);
-                         if (GATED) ptx::tmem_load32(tbase + p.bn / 2 + at + h * 32, u);
-                       },
-                       [&] { if (col + UC >= col_end) release(); });
-          if (!ok) break;
+          process(un & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
+                  [&](int h, float (&z)[32], float (&u)[32]) {
+                    ptx::tmem_load32(tbase + at + h * 32, z);
+                    if (GATED) ptx::tmem_load32(tbase + p.bn / 2 + at + h * 32, u);
+                  },
+                  [&] { if (col + UC >= col_end) release(); });
           if (Cf::LOADS && col + nboxes * UC < col_end)
-            fetch(un & (nboxes - 1), col + nboxes * UC, box_row);
+            fetch(un & (nboxes - 1), jb.c_cols, col + nboxes * UC, box_row);
         }
-        if (!ok) break;
       }
     }
   }
@@ -828,21 +833,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int b = piece + split * (half + 2 * n);
         const int col = tp.tn * cols + b * UC;
         if (col >= col_end) break;
-        const bool ok = process(n & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
-                                [&](int h, float (&z)[32], float (&u)[32]) {
-                                  gather(b * UC + h * 32, z);
-                                  if (GATED) gather(p.bn / 2 + b * UC + h * 32, u);
-                                },
-                                [] {});
-        if (!ok) break;
+        process(n & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
+                [&](int h, float (&z)[32], float (&u)[32]) {
+                  gather(b * UC + h * 32, z);
+                  if (GATED) gather(p.bn / 2 + b * UC + h * 32, u);
+                },
+                [] {});
         const int next = col + nboxes * 2 * split * UC;
-        if (Cf::LOADS && next < col_end) fetch(n & (nboxes - 1), next, box_row);
+        if (Cf::LOADS && next < col_end) fetch(n & (nboxes - 1), jb.c_cols, next, box_row);
       }
     }
   }
   if (warp >= 2) {
-    for (int i = 0; i < nboxes; ++i)
-      if ((in_flight >> i) & 1u) wait_bar_drain(box_bar(i), (box_ph >> i) & 1u, 100000000ull);
+    if (Cf::LOADS) ptx::copy_wait<0>();
     if (lane == 0) ptx::bulk_wait<0>();  // this warp's output stores have landed
     __syncwarp();
   }
@@ -1095,8 +1098,8 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   p.bias = g.bias;
   p.m_rows = g.M;
   const void* d = dz ? g.D : (mode == FFN_LINEAR ? g.R : nullptr);
-  if (d && !make_map(&maps.d, d, g.Ncols, g.M, dz ? g.ldd : g.ldr, uc, 32, F32, 2, 1, 0, "D"))
-    return cudaErrorInvalidResourceHandle;
+  p.d = static_cast<const char*>(d);
+  p.d_stride = (dz ? g.ldd : g.ldr) * (F32 ? 4 : 2);
   if (dz && F32) {
     p.parts[0] = static_cast<__nv_bfloat16*>(g.C);
     p.parts[1] = static_cast<__nv_bfloat16*>(g.C2);

@@ -6,7 +6,7 @@
 // (D[128 features x nt tokens] = W_tile X^T, nt = N rounded up to 16, the tokens past N zero-filled
 // by TMA), so one kernel serves one token and a hundred at the same bytes.
 //   warp 0      TMA producer: k-blocks of 64 of the weight rows (of Wg and Wu both) and of X through
-//               a ring of about 100 KB, two CTAs per SM: 200 KB in flight per SM
+//               a ring of up to 218 KB, or two CTAs per SM of 110 KB: 200 KB in flight per SM
 //   warp 1      MMA issuer (tcgen05, cta_group::1, M = 128, N = nt), accumulators in TMEM
 //   warps 2..5  epilogue: thread = feature, so a token's results leave as 64 contiguous bytes a warp
 // With few row tiles the K loop is split over a cluster of S = 2, 4 or 8 CTAs; each puts its fp32
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int BK = 64;
 constexpr int THREADS = 192;
-constexpr int MAX_STAGES = 8;
+constexpr int MAX_STAGES = 12;
 constexpr int CTL_BYTES = 256;
 constexpr int MAX_SPLIT = 8;
 constexpr int W_BYTES = BM * 128;  // one k-block of 128 weight rows
@@ -291,22 +291,26 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>(W * p.nt)) p.tmem_cols *= 2;
   p.stage_bytes = W * W_BYTES + p.nt * 128;
-  // Two CTAs per SM while two k-blocks fit in half its shared memory and the accumulators in half its
-  // tensor memory, else one.  (The CTAs an SM holds never need more than its 512 columns together: a
-  // CTA of a cluster that waited for them could be waited for in turn.)
-  const bool two = 2 * p.stage_bytes + 1024 + CTL_BYTES <= SMEM_TWO && p.tmem_cols <= 256;
-  const int budget = (two ? SMEM_TWO : SMEM_ONE) - 1024 - CTL_BYTES;
-  p.stages = std::min(MAX_STAGES, budget / p.stage_bytes);
-  p.ring_bytes = p.stages * p.stage_bytes;
-  // Split K until those places are filled, keeping at least four k-blocks for each CTA and the partial
-  // sums of a tile within the budget.
+  // Tiles for more than half the SMs but not more than one each: one CTA per SM with a deep ring and its
+  // whole K loop (48 x 6144 x 16384 gated: 64 us, 70 with 256 CTAs on half the ring and half of K each;
+  // 128 x 4096 x 11008: 40 and 58).  Otherwise two CTAs per SM, where two k-blocks fit in half its shared
+  // memory and the accumulators in half its tensor memory, and K split until those places are filled,
+  // with at least four k-blocks for each CTA and the partial sums of a tile within the budget.  (The
+  // CTAs an SM holds never need more than its 512 columns together: a CTA of a cluster that waited for
+  // them could be waited for in turn.)
   const int64_t tiles = (g.Ncols + BM - 1) / BM;
+  const bool one_each = 2 * tiles > num_sms && tiles <= num_sms;
+  const bool two = !one_each && 2 * p.stage_bytes + 1024 + CTL_BYTES <= SMEM_TWO &&
+                   p.tmem_cols <= 256;
+  const int budget = (two ? SMEM_TWO : SMEM_ONE) - 1024 - CTL_BYTES;
   const int64_t places = (two ? 2 : 1) * num_sms;
   const int part_bytes = W * p.N * BM * 4;
   p.split = 1;
   while (p.split < MAX_SPLIT && part_bytes <= budget && tiles * p.split * 2 <= places &&
          p.nkb >= 8 * p.split)
     p.split *= 2;
+  p.stages = std::min(MAX_STAGES, budget / p.stage_bytes);
+  p.ring_bytes = p.stages * p.stage_bytes;
   if (p.split > 1) p.ring_bytes = std::max(p.ring_bytes, part_bytes);
   Maps maps;
   memset(&maps, 0, sizeof(maps));

@@ -57,12 +57,10 @@ struct FfnTc {
   int64_t part_stride;
 };
 
-// State of a call between its launches (each updates it): what is known to be zero in the workspace
-// header.
+// What a call knows to be zero in the workspace header, updated by each launch.
 struct CallState {
   bool flags = false;  // the error flags
   bool sched = false;  // the scheduler counters
-  bool dependent = false;  // the stream's last kernel is this call's: the next may be a dependent launch
 };
 
 // Tensor cores: lce_ffn_tc.cu.  Several jobs only for FFN_GRADS, where a job whose C is null is not
@@ -87,9 +85,8 @@ cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStr
 // Few tokens, fp32: lce_ffn_simt.cu.  Clears the error flags.
 cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream);
 // out[c] = sum over the N rows of x[., c], row stride ld.  parts = 1: x and out bf16; parts = 3: x
-// holds three bf16 parts, part_stride apart, and out is fp32; dependent: the stream's last kernel is
-// this call's: lce_ffn_simt.cu
+// holds three bf16 parts, part_stride apart, and out is fp32: lce_ffn_simt.cu
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
-                              int64_t part_stride, void* out, bool dependent, cudaStream_t stream);
+                              int64_t part_stride, void* out, cudaStream_t stream);
 
 }  // namespace lce

@@ -129,7 +129,7 @@ struct Call {
   }
   cudaError_t pack_all() {
     if (npack == 0) return cudaSuccess;
-    state.flags = state.sched = state.dependent = true;  // the launch clears the header
+    state.flags = state.sched = true;  // the launch clears the header
     return traced(K_PACK, stream,
                   [&] { return launch_pack(pack, npack, dt == LCE_BF16 ? 1 : 3, flags(), stream); });
   }
@@ -268,10 +268,9 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
   }
   if (dbias && traced(K_COLSUM, stream, [&] {
         return launch_column_sum(z.ptr, z.ld, N, d_out, static_cast<int>(z.parts), z.part_stride,
-                                 dbias, c.state.dependent, stream);
+                                 dbias, stream);
       }) != cudaSuccess)
     return LCE_ERR_CUDA;
-  if (dbias) c.state.dependent = true;
   if (products(c, x, &w, &z, 1, N, d_in, d_out, dX, &dW) != cudaSuccess) return LCE_ERR_CUDA;
   // no launch that clears the error flags (dbias alone, or nothing asked for)
   if (!c.state.flags && zero(workspace, WS_HEADER_BYTES, stream) != cudaSuccess) return LCE_ERR_CUDA;

@@ -92,9 +92,6 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / p.split);
 
   if (threadIdx.x == 0) {
-    // The workspace's error flags: the first CTA is among the first to run, and a wait gives up only
-    // WAIT_LIMIT_NS after that.
-    if (blockIdx.x == 0) *p.err = 0u;
     for (int s = 0; s < p.stages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
@@ -108,6 +105,15 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&maps.w);
+    ptx::prefetch_tmap(&maps.x);
+    if (GATED) ptx::prefetch_tmap(&maps.w2);
+  }
+  ptx::wait_for_previous();  // no memory of the caller is touched before this
+  // The workspace's error flags: the first CTA is among the first to run, and a wait gives up only
+  // WAIT_LIMIT_NS after that.
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0u;
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
@@ -129,6 +135,8 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
         ptx::tma_load_2d(s0 + x_off, &maps.x, kb * BK, 0, full);
         if (++r.stage == p.stages) { r.stage = 0; r.ph ^= 1u; }
       }
+      // only now: CTAs of the next launch that came earlier would take places next to slower ones of this
+      ptx::launch_dependents();
       if (!ok) {  // let copies already in flight land before the CTA can exit
         const uint64_t t0 = ptx::globaltimer();
         while (ptx::globaltimer() - t0 < 2000000ull) {}
@@ -323,13 +331,14 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = p.ring_bytes + 1024 + CTL_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1] = dependent_launch();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATED>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)

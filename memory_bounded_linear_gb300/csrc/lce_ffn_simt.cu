@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
   constexpr int ROWS = GATED ? 2 : 4, R = 4;
   __shared__ float sh[WARPS][R * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::wait_for_previous();  // no memory of the caller is touched before this
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0u;  // this kernel never waits
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * ROWS;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * NT;
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
         acc[r][t] = fmaf(wv[r].x, xv.x, fmaf(wv[r].y, xv.y, fmaf(wv[r].z, xv.z, fmaf(wv[r].w, xv.w, acc[r][t]))));
     }
   }
+  ptx::launch_dependents();
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -92,12 +94,14 @@ template <bool GATED>
 cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
   constexpr int ROWS = GATED ? 2 : 4;
   const unsigned bx = static_cast<unsigned>((g.Ncols + ROWS - 1) / ROWS);
-  const auto by = [&](int nt) { return dim3(bx, static_cast<unsigned>((g.M + nt - 1) / nt)); };
-  if (g.M == 1) few_f32_kernel<1, GATED><<<by(1), WARPS * 32, 0, stream>>>(g, err);
-  else if (g.M == 2) few_f32_kernel<2, GATED><<<by(2), WARPS * 32, 0, stream>>>(g, err);
-  else if (g.M <= 4) few_f32_kernel<4, GATED><<<by(4), WARPS * 32, 0, stream>>>(g, err);
-  else few_f32_kernel<8, GATED><<<by(8), WARPS * 32, 0, stream>>>(g, err);
-  return cudaGetLastError();
+  auto launch = [&](auto kernel, int nt) {
+    const dim3 grid(bx, static_cast<unsigned>((g.M + nt - 1) / nt));
+    return launch_kernel(kernel, grid, WARPS * 32, stream, g, err);
+  };
+  if (g.M == 1) return launch(few_f32_kernel<1, GATED>, 1);
+  if (g.M == 2) return launch(few_f32_kernel<2, GATED>, 2);
+  if (g.M <= 4) return launch(few_f32_kernel<4, GATED>, 4);
+  return launch(few_f32_kernel<8, GATED>, 8);
 }
 
 // ---------------------------------------------------------------------------- column sums
@@ -121,7 +125,6 @@ template <int PARTS, typename O>
 __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
     column_sum_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t part_stride, int64_t N,
                       int64_t cols, O* __restrict__ out) {
-  ptx::launch_dependents();
   ptx::wait_for_previous();
   __shared__ float sh[WARPS][SUM_COLS];
   __shared__ float total[SUM_COLS];
@@ -160,6 +163,7 @@ __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
       for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
   }
+  ptx::launch_dependents();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     s[i] += __shfl_xor_sync(0xffffffffu, s[i], 16);
@@ -201,7 +205,7 @@ struct PackParams {
 template <int PARTS>
 __global__ void __launch_bounds__(WARPS * 32) pack_kernel(const __grid_constant__ PackParams p) {
   constexpr int VEC = PARTS == 3 ? 4 : 8;  // elements per 16 bytes read
-  ptx::launch_dependents();
+  ptx::wait_for_previous();  // no memory of the caller is touched before this
   if (blockIdx.x == 0 && threadIdx.x < WS_HEADER_BYTES / 4) p.header[threadIdx.x] = 0u;
   int k = 0;
   while (k + 1 < p.count && p.first[k + 1] <= blockIdx.x) ++k;
@@ -222,6 +226,7 @@ __global__ void __launch_bounds__(WARPS * 32) pack_kernel(const __grid_constant_
       v[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) +
                                              (row[u] * a.ld + col[u]) * (16 / VEC));
   }
+  ptx::launch_dependents();
 #pragma unroll
   for (int u = 0; u < PACK_UNROLL; ++u) {
     if (row[u] >= a.rows) break;
@@ -251,23 +256,14 @@ cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t str
 }
 
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
-                              int64_t part_stride, void* out, bool dependent, cudaStream_t stream) {
+                              int64_t part_stride, void* out, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((cols + SUM_COLS - 1) / SUM_COLS * SUM_SPLIT);
   const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(WARPS * 32, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0] = dependent_launch();
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  const cudaError_t e =
-      parts == 3 ? cudaLaunchKernelEx(&cfg, column_sum_kernel<3, float>, h, ld, part_stride, N, cols,
-                                      static_cast<float*>(out))
-                 : cudaLaunchKernelEx(&cfg, column_sum_kernel<1, __nv_bfloat16>, h, ld, int64_t(0), N,
-                                      cols, static_cast<__nv_bfloat16*>(out));
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  const dim3 grid(blocks);
+  return parts == 3 ? launch_kernel(column_sum_kernel<3, float>, grid, WARPS * 32, stream, h, ld,
+                                    part_stride, N, cols, static_cast<float*>(out))
+                    : launch_kernel(column_sum_kernel<1, __nv_bfloat16>, grid, WARPS * 32, stream, h, ld,
+                                    int64_t(0), N, cols, static_cast<__nv_bfloat16*>(out));
 }
 
 cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned* header,
@@ -286,9 +282,9 @@ cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned*
     set_error_detail("operand copy of %lld blocks: beyond a launch's grid", static_cast<long long>(blocks));
     return cudaErrorInvalidValue;
   }
-  if (parts == 3) pack_kernel<3><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
-  else pack_kernel<1><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return parts == 3 ? launch_kernel(pack_kernel<3>, grid, WARPS * 32, stream, p)
+                    : launch_kernel(pack_kernel<1>, grid, WARPS * 32, stream, p);
 }
 
 }  // namespace lce

@@ -458,8 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ptx::prefetch_tmap(&maps.b[j][0]);
     }
   }
-  ptx::launch_dependents();
-  ptx::wait_for_previous();  // the operands may come from the previous launch of this call
+  ptx::wait_for_previous();  // no memory of the caller is touched before this
   // the first CTA is among the first to run, and a wait gives up only WAIT_LIMIT_NS after that
   if (threadIdx.x == 0 && blockIdx.x == 0 && p.clear_flags) *p.err = 0u;
   ptx::cluster_sync();
@@ -629,6 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
+      ptx::launch_dependents();
       if (!ok) {
         // Let copies already in flight land before the CTA can exit.
         const uint64_t t0 = ptx::globaltimer();
@@ -996,7 +996,7 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
 }
 
 template <int MODE, bool F32>
-cudaError_t launch(const FMaps& maps, KParams& p, bool dependent, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stream) {
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
@@ -1027,7 +1027,7 @@ cudaError_t launch(const FMaps& maps, KParams& p, bool dependent, int num_sms, c
   attr[0].val.clusterDim.z = 1;
   attr[1] = dependent_launch();
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, true>, maps, p)
                               : cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, false>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -1120,21 +1120,18 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
                                       stream);
       if (e != cudaSuccess) return e;
       state->flags = state->sched = true;  // the launch leaves the counters at zero
-      state->dependent = false;
     }
   }
-  const bool dependent = state->dependent;
-  state->dependent = true;
   p.clear_flags = !state->flags;
   state->flags = true;
   switch (mode) {
     case FFN_LINEAR:
-      return d ? launch<FFN_LINEAR_RES, F32>(maps, p, dependent, num_sms, stream)
-               : launch<FFN_LINEAR, F32>(maps, p, dependent, num_sms, stream);
-    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, dependent, num_sms, stream);
-    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, dependent, num_sms, stream);
-    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, dependent, num_sms, stream);
-    default: return launch<FFN_GRADS, F32>(maps, p, dependent, num_sms, stream);
+      return d ? launch<FFN_LINEAR_RES, F32>(maps, p, num_sms, stream)
+               : launch<FFN_LINEAR, F32>(maps, p, num_sms, stream);
+    case FFN_GATED: return launch<FFN_GATED, F32>(maps, p, num_sms, stream);
+    case FFN_LINEAR_DZ: return launch<FFN_LINEAR_DZ, F32>(maps, p, num_sms, stream);
+    case FFN_GATED_DGU: return launch<FFN_GATED_DGU, F32>(maps, p, num_sms, stream);
+    default: return launch<FFN_GRADS, F32>(maps, p, num_sms, stream);
   }
 }
 

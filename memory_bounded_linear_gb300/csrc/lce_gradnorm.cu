@@ -20,6 +20,7 @@
 
 #include "lce.h"
 #include "lce_internal.h"
+#include "ptx.cuh"
 
 namespace lce {
 namespace {
@@ -149,6 +150,7 @@ __device__ __forceinline__ Chunk chunk_of(const Table<CAP>& t, int64_t c) {
 template <bool INF, int CAP>
 __global__ void __launch_bounds__(THREADS, 2)
     norm_kernel(const __grid_constant__ Table<CAP> t, double* part) {
+  ptx::wait_for_previous();  // no memory of the caller is touched before this
   double sum = 0.0;
   unsigned m = 0;
   for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     sum += static_cast<double>(a.s);
     m = max(m, a.m);
   }
+  ptx::launch_dependents();
   const double r = reduce<INF>(INF ? static_cast<double>(m) : sum);
   if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
@@ -178,6 +181,7 @@ __device__ __forceinline__ float total_of(const double* part, int parts) {
 
 template <bool INF>
 __global__ void __launch_bounds__(THREADS) total_kernel(const double* part, int parts, float* total) {
+  ptx::wait_for_previous();
   const float v = total_of<INF>(part, parts);
   if (threadIdx.x == 0) *total = v;
 }
@@ -230,6 +234,7 @@ template <bool INF, int CAP>
 __global__ void __launch_bounds__(THREADS, 2)
     scale_kernel(const __grid_constant__ Table<CAP> t, const double* part, int parts, float max_norm,
                  float* total) {
+  ptx::wait_for_previous();
   const float v = total_of<INF>(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *total = v;
   const float q = max_norm / (v + 1e-6f);
@@ -310,8 +315,7 @@ lce_status_t run(const void* const* grads, void* const* out, const int64_t* nume
   cudaError_t e = for_tables<CAP>(grads, out, numels, dtypes, count, [&](const Table<CAP>& t) {
     const int blocks = static_cast<int>(std::min<int64_t>(t.first[t.count], MAX_BLOCKS));
     const cudaError_t r = traced(K_GRAD_NORM, stream, [&] {
-      norm_kernel<INF, CAP><<<blocks, THREADS, 0, stream>>>(t, part + parts);
-      return cudaGetLastError();
+      return launch_kernel(norm_kernel<INF, CAP>, dim3(blocks), THREADS, stream, t, part + parts);
     });
     parts += blocks;
     return r;
@@ -319,16 +323,15 @@ lce_status_t run(const void* const* grads, void* const* out, const int64_t* nume
   if (e != cudaSuccess) return LCE_ERR_CUDA;
   if (!clip || parts == 0) {
     e = traced(K_GRAD_NORM, stream, [&] {
-      total_kernel<INF><<<1, THREADS, 0, stream>>>(part, parts, total);
-      return cudaGetLastError();
+      return launch_kernel(total_kernel<INF>, dim3(1), THREADS, stream, part, parts, total);
     });
     return e == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
   }
   e = for_tables<CAP>(grads, out, numels, dtypes, count, [&](const Table<CAP>& t) {
     const int blocks = static_cast<int>(std::min<int64_t>(t.first[t.count], MAX_BLOCKS));
     return traced(K_GRAD_SCALE, stream, [&] {
-      scale_kernel<INF, CAP><<<blocks, THREADS, 0, stream>>>(t, part, parts, max_norm, total);
-      return cudaGetLastError();
+      return launch_kernel(scale_kernel<INF, CAP>, dim3(blocks), THREADS, stream, t, part, parts,
+                           max_norm, total);
     });
   });
   return e == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;

@@ -96,14 +96,28 @@ struct StripArgs {
 // Kernels a launcher started beyond its first one (the launch counter adds them), per thread.
 extern thread_local int g_extra_kernels;
 
-// Attribute of a dependent launch: its CTAs may start while the previous kernel of the stream drains,
-// and wait for it (ptx::wait_for_previous) before they touch memory.  Only between kernels of one
-// call, each of which either waits or touches nothing that a running predecessor uses.
+// Attribute of a dependent launch: its CTAs may start while the previous kernel of the stream drains.
+// A kernel launched so calls ptx::wait_for_previous, which returns once that kernel has finished and
+// its writes are visible, before it touches any memory of the caller; so it is safe after any kernel.
+// ptx::launch_dependents in a kernel says from where on the next launch may start its CTAs.
 inline cudaLaunchAttribute dependent_launch() {
   cudaLaunchAttribute a{};
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
   return a;
+}
+// A dependent launch of `kernel` without dynamic shared memory.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // Launch bookkeeping (lce_api.cu): trace events around a launch and the launch counter.

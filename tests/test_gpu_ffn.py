@@ -322,6 +322,65 @@ def test_stream_and_graph(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_order_with_other_work_on_the_stream(cuda_lib, captured):
+    """Calls read what a memset, a copy and other kernels before them wrote, and what follows them (a
+    copy, an in-place kernel, the same call again) sees their results: round after round, with inputs
+    that change, on one stream."""
+    N, d, F = 3, 520, 1032
+    x, xs = torch.zeros(N, d, dtype=torch.bfloat16, device="cuda"), _rand(1, "bf16", 6, N, d).cuda()
+    w, wu = _rand(2, "bf16", F, d, std=0.04).cuda(), _rand(3, "bf16", F, d, std=0.04).cuda()
+    wd, b = _rand(4, "bf16", d, F, std=0.03).cuda(), _rand(5, "bf16", d).cuda()
+    h = torch.zeros(N, F, dtype=torch.bfloat16, device="cuda")
+    results = torch.zeros(6, N, d, dtype=torch.bfloat16, device="cuda")
+    grads = [torch.zeros(N, d, device="cuda")]
+
+    def rounds():
+        for k in range(6):
+            x.zero_()
+            x.copy_(xs[k])
+            h.zero_()
+            api.lce_gated_forward(x, w, wu, out=h)
+            api.lce_linear_forward(h, wd, b, x, out=x)
+            x.mul_(0.5)
+            api.lce_gated_forward(x, w, wu, out=h)
+            api.lce_linear_forward(h, wd, b, x, out=results[k])
+            grads[0].copy_(results[k])
+            api.lce_clip_grad_norm(grads, 1.0)
+            results[k].copy_(grads[0])
+    if captured:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            rounds()
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            rounds()
+        xs.mul_(1.5)
+        for _ in range(3):
+            results.fill_(7.0)
+            g.replay()
+    else:
+        for _ in range(3):
+            rounds()
+    torch.cuda.synchronize()
+    for k in range(6):
+        step = xs[k].clone()
+        for i in range(2):
+            torch.cuda.synchronize()
+            hh = api.lce_gated_forward(step, w, wu)[0]
+            torch.cuda.synchronize()
+            step = api.lce_linear_forward(hh, wd, b, step)[0]
+            torch.cuda.synchronize()
+            if i == 0:
+                step.mul_(0.5)
+        gr = step.float()
+        torch.cuda.synchronize()
+        want = api.lce_clip_grad_norm([gr], 1.0)[1][0].bfloat16()
+        assert torch.equal(results[k], want), k
+
+
 def test_refusals_on_the_gpu(cuda_lib):
     x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(96, 64, device="cuda")
     with pytest.raises(TypeError):

@@ -80,7 +80,7 @@ constexpr int MAX_PACK_ARRAYS = 3;
 cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned* header,
                         cudaStream_t stream);
 // Few tokens, bf16 (at most FFN_FEW_TOKENS rows): lce_ffn_few.cu.  Clears the error flags.
-constexpr int64_t FFN_FEW_TOKENS = 128;
+constexpr int64_t FFN_FEW_TOKENS = 160;
 cudaError_t launch_ffn_few(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream);
 // Few tokens, fp32: lce_ffn_simt.cu.  Clears the error flags.
 cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream);

@@ -27,9 +27,22 @@ bool width_ok(int64_t w, lce_dtype_t dt) {
 }
 bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
 
-// Forward products of at most so many tokens run as a weight stream (lce_ffn_few.cu, and for fp32
-// lce_ffn_simt.cu), larger ones on the kernel whose tiles hold 256 tokens.
-bool few_tokens(int64_t N, lce_dtype_t dt) { return N <= (dt == LCE_BF16 ? FFN_FEW_TOKENS : 16); }
+// Whether a forward product of N tokens runs as a weight stream (lce_ffn_few.cu; fp32:
+// lce_ffn_simt.cu) rather than in tiles of 256 tokens (lce_ffn_tc.cu).  us, stream / tiles:
+//   linear 128 x 8192 -> 4096 18 / 24, 128 x 5224 -> 13384 45 / 39, 160 x 11008 -> 4096 24 / 30, 192: 28 / 31;
+//     160 x 4096 -> 11008 26 / 25: the stream cuts long K loops into more pieces
+//   gated 128 x 4096 x 11008 40 / 47, 160: 42 / 47, 192: 49 / 48 (a tile for each of more than half the
+//     SMs, no joining); 48 x 4096 x 8192 27 / 27, 96: 32 / 27 (two sums to join per tile);
+//     96 x 2048 x 1024 8.7 / 11.9, 128: 22 / 12 (its partial sums no longer fit)
+//   fp32 linear 16 x 2048 -> 8192 51 / 63, 33: 115 / 64 (the weights are read again for every 8 tokens)
+bool few_tokens(int64_t N, int64_t d, int64_t width, int weights, lce_dtype_t dt) {
+  if (dt == LCE_F32) return N <= 16;
+  if (N <= 32) return true;
+  if (weights == 1) return N <= 128 || (N <= FFN_FEW_TOKENS && d >= 2 * width);
+  const int64_t tiles = (width + 127) / 128;  // of the stream: feature rows of one CTA
+  if (tiles > 76 && tiles <= 152) return N <= FFN_FEW_TOKENS;
+  return N <= (tiles <= 16 ? 112 : 48);
+}
 
 // Rows of the workspace's arrays start on 128-byte lines.
 int64_t round64(int64_t x) { return (x + 63) & ~int64_t(63); }
@@ -70,7 +83,7 @@ Layout layout(int64_t N, int64_t d, int64_t width, int weights, int nz, bool bac
     s.part_stride = rows * s.ld;
     off += align256(static_cast<size_t>(s.part_stride) * 2 * (dt == LCE_BF16 ? 1 : 3));
   };
-  L.copies = (backward || !few_tokens(N, dt)) &&
+  L.copies = (backward || !few_tokens(N, d, width, weights, dt)) &&
              (dt == LCE_F32 || (k_major && misaligned(d) && copy_pays(N, width * weights)));
   if (L.copies) {
     take(L.x, N, d);
@@ -198,7 +211,7 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
   if (N == 0)  // otherwise the first launch clears the error flags
     return zero(workspace, WS_HEADER_BYTES, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
   Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
-  if (few_tokens(N, dtype)) {
+  if (few_tokens(N, d_in, d_out, 1, dtype)) {
     FfnGemm g{};
     g.mode = FFN_LINEAR;
     g.act = activation;
@@ -304,7 +317,7 @@ lce_status_t lce_gated_forward(const void* X, int64_t ldx, const void* Wg, const
   if (N == 0)  // otherwise the first launch clears the error flags
     return zero(workspace, WS_HEADER_BYTES, stream) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
   Call c{dtype, static_cast<char*>(workspace), num_sms, stream};
-  if (few_tokens(N, dtype)) {
+  if (few_tokens(N, d, F, 2, dtype)) {
     FfnGemm g{};
     g.mode = FFN_GATED;
     g.act = activation;

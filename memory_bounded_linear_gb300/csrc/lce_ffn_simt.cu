@@ -106,11 +106,11 @@ cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------- column sums
 // Bound by reading x once; with few columns by how many rows are in flight.  A cluster of eight blocks
-// takes a strip of 64 columns; each half-warp of its 64 warps reads rows of the strip (128 contiguous
-// bytes), eight at a time: 1,024 rows in flight per strip.  Half-warps meet by shuffles, warps in
-// shared memory, blocks through distributed shared memory, in a fixed order: one launch, no
-// workspace, no atomics.
-constexpr int SUM_COLS = 64;
+// takes a strip of LANES x 4 columns; every LANES lanes of its 64 warps read rows of the strip, eight at a
+// time: with LANES = 16 rows of 128 contiguous bytes and 1,024 of them in flight per strip; with 8,
+// for up to NARROW columns, 2,048.  Lanes meet by shuffles, warps in shared memory, blocks through
+// distributed shared memory, in a fixed order: one launch, no workspace, no atomics.
+constexpr int64_t NARROW = 2048;
 constexpr int SUM_SPLIT = 8;
 constexpr int SUM_UNROLL = 8;
 
@@ -121,22 +121,23 @@ __device__ __forceinline__ void add4(float (&s)[4], const uint2& q) {
   s[3] += __uint_as_float(q.y & 0xffff0000u);
 }
 
-template <int PARTS, typename O>
+template <int PARTS, int LANES, typename O>
 __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
     column_sum_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t part_stride, int64_t N,
                       int64_t cols, O* __restrict__ out) {
+  constexpr int SUM_COLS = LANES * 4, PER_WARP = 32 / LANES;  // columns; rows a warp reads at once
   ptx::wait_for_previous();
   __shared__ float sh[WARPS][SUM_COLS];
   __shared__ float total[SUM_COLS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % SUM_SPLIT;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x / SUM_SPLIT) * SUM_COLS;
-  const int64_t c = c0 + (lane & 15) * 4;
+  const int64_t c = c0 + (lane & (LANES - 1)) * 4;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < cols) {
-    constexpr int64_t STEP = SUM_SPLIT * WARPS * 2;
+    constexpr int64_t STEP = SUM_SPLIT * WARPS * PER_WARP;
     const int64_t step = STEP * ld;
-    int64_t r = (rank * WARPS + warp) * 2 + (lane >> 4);
+    int64_t r = (rank * WARPS + warp) * PER_WARP + lane / LANES;
     const __nv_bfloat16* p = x + r * ld + c;
     for (; r + (SUM_UNROLL - 1) * STEP < N; r += SUM_UNROLL * STEP, p += SUM_UNROLL * step) {
       uint2 q[SUM_UNROLL][PARTS];
@@ -166,8 +167,9 @@ __global__ void __cluster_dims__(SUM_SPLIT, 1, 1) __launch_bounds__(WARPS * 32)
   ptx::launch_dependents();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s[i] += __shfl_xor_sync(0xffffffffu, s[i], 16);
-    if (lane < 16) sh[warp][lane * 4 + i] = s[i];
+#pragma unroll
+    for (int o = 16; o >= LANES; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+    if (lane < LANES) sh[warp][lane * 4 + i] = s[i];
   }
   __syncthreads();
   if (threadIdx.x < SUM_COLS) {
@@ -257,13 +259,19 @@ cudaError_t launch_ffn_few_f32(const FfnGemm& g, unsigned* err, cudaStream_t str
 
 cudaError_t launch_column_sum(const void* x, int64_t ld, int64_t N, int64_t cols, int parts,
                               int64_t part_stride, void* out, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>((cols + SUM_COLS - 1) / SUM_COLS * SUM_SPLIT);
   const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
-  const dim3 grid(blocks);
-  return parts == 3 ? launch_kernel(column_sum_kernel<3, float>, grid, WARPS * 32, stream, h, ld,
-                                    part_stride, N, cols, static_cast<float*>(out))
-                    : launch_kernel(column_sum_kernel<1, __nv_bfloat16>, grid, WARPS * 32, stream, h, ld,
-                                    int64_t(0), N, cols, static_cast<__nv_bfloat16*>(out));
+  auto launch = [&](auto kernel, int strip, auto* result) {
+    const dim3 grid(static_cast<unsigned>((cols + strip - 1) / strip * SUM_SPLIT));
+    return launch_kernel(kernel, grid, WARPS * 32, stream, h, ld, part_stride, N, cols, result);
+  };
+  if (parts == 3) {
+    float* o = static_cast<float*>(out);
+    return cols <= NARROW ? launch(column_sum_kernel<3, 8, float>, 32, o)
+                          : launch(column_sum_kernel<3, 16, float>, 64, o);
+  }
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  return cols <= NARROW ? launch(column_sum_kernel<1, 8, __nv_bfloat16>, 32, o)
+                        : launch(column_sum_kernel<1, 16, __nv_bfloat16>, 64, o);
 }
 
 cudaError_t launch_pack(const PackArray* arrays, int count, int parts, unsigned* header,

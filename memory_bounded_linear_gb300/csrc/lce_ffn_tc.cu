@@ -934,6 +934,7 @@ int max_clusters(int pairs) {
 struct Plan {
   int bn = TILE, split = 1;
   bool whole[MAX_JOBS] = {};
+  double cost = 0.0;  // estimate, SM cycles
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -946,7 +947,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <bool F32>
 Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
   Plan best;
-  double best_cost = 0.0;
   for (int bn = TILE; bn >= TILE / 2; bn /= 2) {
     const double step_cost = (bn == TILE ? 528.0 : 390.0) * (F32 ? 6 * F32_STEP : 1);
     const double finish = 3000.0 * bn / TILE * (F32 ? 2 : 1);
@@ -965,10 +965,10 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
                   : njobs == 1 ? ceil_div(all, units) * longest
                                : work / units + longest / 2;
     cost += finish;
-    if (best_cost == 0.0 || cost < best_cost) {
-      best_cost = cost;
+    if (best.cost == 0.0 || cost < best.cost) {
       best = Plan{};
       best.bn = bn;
+      best.cost = cost;
     }
     for (int k = 2; k <= MAX_SPLIT; k *= 2) {
       // products are cut from `least` steps per piece on; the others' tiles lie side by side
@@ -984,8 +984,8 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
           slowest = std::max(slowest, whole[j] ? ceil_div(steps[j], k) * step_cost + join + finish / k
                                                : steps[j] * step_cost + finish);
         }
-        if (!any || clusters > max_clusters<F32>(k) || slowest >= best_cost) continue;
-        best_cost = slowest;
+        if (!any || clusters > max_clusters<F32>(k) || slowest >= best.cost) continue;
+        best.cost = slowest;
         best.bn = bn;
         best.split = k;
         for (int j = 0; j < njobs; ++j) best.whole[j] = whole[j];
@@ -1038,8 +1038,8 @@ cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stre
 }
 
 template <bool F32>
-cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state, int num_sms,
-                cudaStream_t stream) {
+cudaError_t run(const FfnTc* jobs, int njobs, const Plan& plan, unsigned* header, CallState* state,
+                int num_sms, cudaStream_t stream) {
   FMaps maps;
   memset(&maps, 0, sizeof(maps));
   KParams p{};
@@ -1047,9 +1047,6 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   const bool gated = mode == FFN_GATED || mode == FFN_GATED_DGU;
   const bool dz = mode == FFN_LINEAR_DZ || mode == FFN_GATED_DGU;
   const uint32_t uc = F32 ? 32 : 64;
-  for (int i = 0; i < njobs; ++i)
-    if (ceil_div(jobs[i].K, BK) > (1 << 25)) return cudaErrorInvalidValue;  // widths end at 2^31
-  const Plan plan = choose_plan<F32>(jobs, njobs, gated, num_sms / 2);
   p.split = plan.split;
   p.bn = plan.bn;
   int64_t longest = 0;
@@ -1135,13 +1132,52 @@ cudaError_t run(const FfnTc* jobs, int njobs, unsigned* header, CallState* state
   }
 }
 
+// A launch of all products, or one of the weight gradients and one of the others: sums over very many
+// tokens make few and long tiles, which only a launch of their own can cut for all SMs (backward of
+// 16384 x 512 -> 1024: 8 tiles of 256 k-blocks beside 128 of 16).
+template <bool F32>
+cudaError_t run_planned(const FfnTc* jobs, int njobs, unsigned* header, CallState* state, int num_sms,
+                        cudaStream_t stream) {
+  constexpr double kLaunch = 5000.0;  // cycles that another launch costs
+  const bool gated = jobs[0].mode == FFN_GATED || jobs[0].mode == FFN_GATED_DGU;
+  for (int i = 0; i < njobs; ++i)
+    if (ceil_div(jobs[i].K, BK) > (1 << 25)) return cudaErrorInvalidValue;  // widths end at 2^31
+  const Plan all = choose_plan<F32>(jobs, njobs, gated, num_sms / 2);
+  if (njobs > 1) {
+    FfnTc group[2][MAX_JOBS];
+    int n[2] = {0, 0};
+    for (int i = 0; i < njobs; ++i) {
+      const int k = jobs[i].a_mn ? 0 : 1;
+      group[k][n[k]++] = jobs[i];
+    }
+    if (n[0] && n[1]) {
+      const Plan plan[2] = {choose_plan<F32>(group[0], n[0], gated, num_sms / 2),
+                            choose_plan<F32>(group[1], n[1], gated, num_sms / 2)};
+      if (plan[0].cost + plan[1].cost + kLaunch < all.cost) {
+        int launches = 0;
+        for (int k = 0; k < 2; ++k) {
+          bool asked = false;
+          for (int i = 0; i < n[k]; ++i) asked |= group[k][i].C != nullptr;
+          if (!asked) continue;
+          const cudaError_t e = run<F32>(group[k], n[k], plan[k], header, state, num_sms, stream);
+          if (e != cudaSuccess) return e;
+          ++launches;
+        }
+        g_extra_kernels += launches - 1;
+        return cudaSuccess;
+      }
+    }
+  }
+  return run<F32>(jobs, njobs, all, header, state, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_ffn_tc(const FfnTc* jobs, int njobs, lce_dtype_t dtype, unsigned* header,
                           CallState* state, int num_sms, cudaStream_t stream) {
   if (njobs < 1 || njobs > MAX_JOBS) return cudaErrorInvalidValue;
-  return dtype == LCE_BF16 ? run<false>(jobs, njobs, header, state, num_sms, stream)
-                           : run<true>(jobs, njobs, header, state, num_sms, stream);
+  return dtype == LCE_BF16 ? run_planned<false>(jobs, njobs, header, state, num_sms, stream)
+                           : run_planned<true>(jobs, njobs, header, state, num_sms, stream);
 }
 
 }  // namespace lce

@@ -236,17 +236,21 @@ lce_status_t lce_forward_static_scratch(const void* H, const void* W, const int6
  * gradients behind it.
  *
  * Conventions of the entry points below, beyond those at the top of this file
- *   - dtype is LCE_BF16 (bf16 arrays, fp32 accumulation) or LCE_F32 (fp32 arrays, products and
- *     sums accurate to fp32); every array of a call, gradients included, has that type.  Sums and
- *     the activation are fp32; each result is rounded once.
+ *   - dtype is LCE_BF16 (bf16 arrays, fp32 accumulation) or LCE_F32 (fp32 arrays; products as six
+ *     tensor-core products of three bf16 parts per operand, or fp32 FMAs, accurate to fp32 either
+ *     way); every array of a call, gradients included, has that type.  Sums and the activation are
+ *     fp32; each result is rounded once.
  *   - Weights, biases and weight gradients are dense; X, residual, Y and dY have row strides
  *     (elements) at least their width, so slices of wider arrays can be passed.
  *   - Shape rules (LCE_ERR_UNSUPPORTED_SHAPE otherwise): N >= 0 (N = 0: nothing is written but
  *     zero weight gradients), widths >= 1 whose rows are multiples of 16 bytes (multiples of 8 for
- *     LCE_BF16, of 4 for LCE_F32), row strides likewise; all < 2^31.  Every pointer is 16-byte
- *     aligned; outputs do not overlap inputs, except Y == residual with equal strides.
- *   - The workspace is at least the size its function names; nothing in it is kept between calls.
- *     lce_check_error on it reports a wait that timed out.
+ *     LCE_BF16, of 4 for LCE_F32), row strides likewise; all at most 2^31 - 512, and products of two
+ *     of N and the widths at most 2^48.  Every pointer is 16-byte aligned; outputs do not overlap
+ *     inputs, except Y == residual with equal strides.
+ *   - The workspace is at least the size its function names: 256 bytes for bf16 forward passes; a
+ *     backward pass adds its pre-activations' gradients, fp32 and widths that are no multiple of 16
+ *     copies of operands.  Nothing in it is kept between calls.  lce_check_error on it reports a wait
+ *     that timed out.
  *   - Outputs are bitwise reproducible for a fixed device and fixed shapes.  A row of Y or H does
  *     not depend on the other rows' values, but its summation order may differ between the call
  *     for a few tokens and the call for many.

@@ -112,14 +112,15 @@ def native():
     """The binding of the feed-forward and clipping entry points to torch tensors (built in-tree
     beside liblce.so); raises if it is not there."""
     global _native
-    if _native is None:
-        load()
-        try:
-            from . import _native as module
-        except ImportError as e:
-            raise RuntimeError("_native.so is not built; run `python -c 'import __graft_entry__ as "
-                               "g; g.build()'`") from e
-        _native = module
+    if _native is not None:
+        return _native
+    load()
+    try:
+        from . import _native as module
+    except ImportError as e:
+        raise RuntimeError("_native.so is not built; run `python -c 'import __graft_entry__ as g; "
+                           "g.build()'`") from e
+    _native = module
     return _native
 
 

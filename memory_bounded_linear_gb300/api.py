@@ -256,10 +256,9 @@ def _activation(name: str) -> int:
 # The calls below are made once per layer and token, where the host's time is the call's time: the
 # checks of tensors, the allocations and the C call are in the native binding (csrc/py_binding.cpp).
 
-def _call(what: str, name: str, stream: Optional[torch.cuda.Stream], *args):
-    """native.<name>(*args) on the current stream, or with ``stream`` made current: then what is
-    allocated inside belongs to the stream that the call's kernels run on."""
-    f = getattr(_lib.native(), name)
+def _call(what: str, f, stream: Optional[torch.cuda.Stream], *args):
+    """f(*args) with ``stream`` made current, if one is given: then what is allocated inside belongs
+    to the stream that the call's kernels run on."""
     if stream is None:
         r = f(*args)
     else:
@@ -296,7 +295,7 @@ def lce_linear_forward(X, W, bias=None, residual=None, *, activation: str = "non
     """Y = act(X W^T + bias) + residual.  X [N, d_in], residual and out [N, d_out] may have a row
     stride; W [d_out, d_in] and bias [d_out] are contiguous.  out may be residual itself.
     Returns (Y, workspace)."""
-    return _call("lce_linear_forward", "linear_forward", stream, X, W, bias, residual,
+    return _call("lce_linear_forward", _lib.native().linear_forward, stream, X, W, bias, residual,
                  _activation(activation), out, workspace)
 
 
@@ -306,7 +305,7 @@ def lce_linear_backward(X, W, bias, dY, *, activation: str = "none", parts: str 
     """Gradients of lce_linear_forward (the residual's is dY itself).  ``parts``: "dx", "dw"
     (weights and bias) or "both".  Returns (dX, dW, dbias, workspace); dbias is None without a
     bias, and what ``parts`` leaves out is None."""
-    return _call("lce_linear_backward", "linear_backward", stream, X, W, bias, dY,
+    return _call("lce_linear_backward", _lib.native().linear_backward, stream, X, W, bias, dY,
                  _activation(activation), *_parts(parts), workspace)
 
 
@@ -315,8 +314,8 @@ def lce_gated_forward(X, Wg, Wu, *, activation: str = "silu", out: Optional[torc
                       stream: Optional[torch.cuda.Stream] = None):
     """H = act(X Wg^T) * (X Wu^T).  X [N, d] and out [N, F] may have a row stride; Wg and Wu [F, d]
     are contiguous.  Returns (H, workspace)."""
-    return _call("lce_gated_forward", "gated_forward", stream, X, Wg, Wu, _activation(activation),
-                 out, workspace)
+    return _call("lce_gated_forward", _lib.native().gated_forward, stream, X, Wg, Wu,
+                 _activation(activation), out, workspace)
 
 
 def lce_gated_backward(X, Wg, Wu, dH, *, activation: str = "silu", parts: str = "both",
@@ -324,7 +323,7 @@ def lce_gated_backward(X, Wg, Wu, dH, *, activation: str = "silu", parts: str = 
                        stream: Optional[torch.cuda.Stream] = None):
     """Gradients of lce_gated_forward.  ``parts``: "dx", "dw" (both weights) or "both".  Returns
     (dX, dWg, dWu, workspace); what ``parts`` leaves out is None."""
-    return _call("lce_gated_backward", "gated_backward", stream, X, Wg, Wu, dH,
+    return _call("lce_gated_backward", _lib.native().gated_backward, stream, X, Wg, Wu, dH,
                  _activation(activation), *_parts(parts), workspace)
 
 
@@ -435,7 +434,8 @@ def lce_grad_norm(grads: Sequence[torch.Tensor], *, norm: str = "l2",
                   stream: Optional[torch.cuda.Stream] = None):
     """Global norm ("l2" or "inf") of a non-empty list of gradients (bfloat16 and float32 mixed,
     each dense).  Returns (total [] fp32 on the device, workspace)."""
-    return _call("lce_grad_norm", "clip", stream, grads, None, _norm(norm), None, workspace)
+    return _call("lce_grad_norm", _lib.native().clip, stream, grads, None, _norm(norm), None,
+                 workspace)
 
 
 def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: str = "l2",
@@ -449,7 +449,7 @@ def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: 
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)
-    total, ws = _call("lce_clip_grad_norm", "clip", stream, grads, out, _norm(norm),
+    total, ws = _call("lce_clip_grad_norm", _lib.native().clip, stream, grads, out, _norm(norm),
                       float(max_norm), workspace)
     return total, list(grads if out is None else out), ws
 

@@ -12,7 +12,10 @@
 namespace lce {
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Tiles are addressed with 32-bit coordinates, the last one a tile's width past the end at most; sizes
+// of arrays stay far from 64 bits.
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;
+constexpr int64_t kMaxElements = int64_t(1) << 48;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -26,6 +29,10 @@ bool width_ok(int64_t w, lce_dtype_t dt) {
   return w >= mult && w % mult == 0 && w <= kMaxDim;
 }
 bool rows_ok(int64_t N) { return N >= 0 && N <= kMaxDim; }
+bool sizes_ok(int64_t N, int64_t d, int64_t width, lce_dtype_t dt) {
+  return rows_ok(N) && width_ok(d, dt) && width_ok(width, dt) && N * d <= kMaxElements &&
+         N * width <= kMaxElements && d * width <= kMaxElements;
+}
 
 // Whether a forward product of N tokens runs as a weight stream (lce_ffn_few.cu; fp32:
 // lce_ffn_simt.cu) rather than in tiles of 256 tokens (lce_ffn_tc.cu).  us, stream / tiles:
@@ -184,7 +191,7 @@ extern "C" {
 size_t lce_linear_workspace_size(int64_t N, int64_t d_in, int64_t d_out, lce_activation_t activation,
                                  int32_t backward, lce_dtype_t dtype) {
   if (!dtype_ok(dtype) || !act_ok(activation) || (backward != 0 && backward != 1)) return 0;
-  if (!rows_ok(N) || !width_ok(d_in, dtype) || !width_ok(d_out, dtype)) return 0;
+  if (!sizes_ok(N, d_in, d_out, dtype)) return 0;
   return linear_layout(N, d_in, d_out, activation, backward != 0, dtype).total;
 }
 
@@ -293,7 +300,7 @@ lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, cons
 size_t lce_gated_workspace_size(int64_t N, int64_t d, int64_t F, int32_t backward,
                                 lce_dtype_t dtype) {
   if (!dtype_ok(dtype) || (backward != 0 && backward != 1)) return 0;
-  if (!rows_ok(N) || !width_ok(d, dtype) || !width_ok(F, dtype)) return 0;
+  if (!sizes_ok(N, d, F, dtype)) return 0;
   return gated_layout(N, d, F, backward != 0, dtype).total;
 }
 

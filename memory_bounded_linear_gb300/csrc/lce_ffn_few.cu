@@ -274,15 +274,17 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int
 
 template <bool GATED>
 cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
+  static bool attr_set[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<GATED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
     if (e != cudaSuccess) {
       set_error_detail("shared-memory attribute of the few-token kernel: %s", cudaGetErrorName(e));
       return e;
     }
-    attr_set = true;
+    attr_set[dev] = true;
   }
   constexpr int W = GATED ? 2 : 1;
   Params p{};

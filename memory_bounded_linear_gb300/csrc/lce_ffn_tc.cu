@@ -997,8 +997,10 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
 
 template <int MODE, bool F32>
 cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
+  static bool attr_set[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e == cudaSuccess)
@@ -1008,7 +1010,7 @@ cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stre
       set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(e));
       return e;
     }
-    attr_set = true;
+    attr_set[dev] = true;
   }
   int clusters = 0;
   for (int j = 0; j < p.njobs; ++j)

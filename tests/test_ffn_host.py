@@ -53,6 +53,9 @@ def test_workspace_size_refusals(lib):
     assert lib.lce_linear_workspace_size(1 << 31, 64, 64, 0, 0, 0) == 0
     assert lib.lce_linear_workspace_size(4, 0, 64, 0, 0, 0) == 0
     assert lib.lce_linear_workspace_size(4, 64, 1 << 31, 0, 0, 0) == 0
+    assert lib.lce_linear_workspace_size((1 << 31) - 511, 64, 64, 0, 0, 0) == 0
+    assert lib.lce_linear_workspace_size(1 << 30, 1 << 30, 64, 0, 0, 1) == 0     # 2^60 elements
+    assert lib.lce_gated_workspace_size(64, 1 << 30, 1 << 30, 1, 0) == 0
     assert lib.lce_linear_workspace_size(4, 64, 64, 5, 0, 0) == 0      # activation
     assert lib.lce_linear_workspace_size(4, 64, 64, -1, 0, 0) == 0
     assert lib.lce_linear_workspace_size(4, 64, 64, 0, 2, 0) == 0      # direction
@@ -61,6 +64,27 @@ def test_workspace_size_refusals(lib):
     assert lib.lce_gated_workspace_size(0, 64, 64, 1, 0) > 0           # no token is allowed
     assert lib.lce_grad_norm_workspace_size(-1) == 0
     assert lib.lce_grad_norm_workspace_size(0) > 0
+
+
+def test_workspace_sizes(lib):
+    """What the workspace holds: the header; the pre-activations' gradients in rows of whole 128-byte
+    lines; for fp32 three bf16 parts of the operands; aligned copies where rows are no multiple of 32
+    bytes and every element enters many products."""
+    r64 = lambda x: (x + 63) // 64 * 64  # noqa: E731
+    r256 = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    H = 256
+    assert lib.lce_linear_workspace_size(5000, 4096, 4096, 3, 0, 0) == H
+    assert lib.lce_linear_workspace_size(5000, 4096, 4096, 0, 1, 0) == H
+    assert lib.lce_linear_workspace_size(5000, 4096, 4104, 3, 1, 0) == H + r256(5000 * r64(4104) * 2)
+    assert lib.lce_gated_workspace_size(300, 64, 200, 1, 0) == H + 2 * r256(300 * r64(200) * 2)
+    copies = r256(5000 * r64(4104) * 2) + r256(4096 * r64(4104) * 2)
+    assert lib.lce_linear_workspace_size(5000, 4104, 4096, 3, 0, 0) == H + copies
+    assert lib.lce_linear_workspace_size(50, 4104, 4096, 3, 0, 0) == H
+    parts = lambda n, c: r256(n * r64(c) * 2 * 3)  # noqa: E731
+    assert lib.lce_linear_workspace_size(8, 100, 200, 3, 0, 1) == H          # few tokens: no parts
+    assert lib.lce_linear_workspace_size(80, 100, 200, 0, 0, 1) == H + parts(80, 100) + parts(200, 100)
+    assert lib.lce_gated_workspace_size(80, 100, 200, 1, 1) == \
+        H + parts(80, 100) + 2 * parts(200, 100) + 2 * parts(80, 200)
 
 
 def _linear(lib, X=P, ldx=64, W=P, b=P, R=P, ldr=96, N=5, di=64, do=96, act=0, dt=0, Y=P + 4096, ldy=96,

@@ -125,6 +125,78 @@ def test_widths_f32(cuda_lib, a, b, N):
     _linear_case("f32", N, a, b, "none", True, False, seed=a + b)
 
 
+def _act64(z, name):
+    if name == "none":
+        return z
+    if name == "silu":
+        return z * torch.sigmoid(z)
+    return 0.5 * z * torch.erfc(-z * 0.5 ** 0.5)
+
+
+def _close(got, want, tol, what):
+    assert torch.isfinite(got).all(), what
+    err = (got.double() - want).norm() / want.norm()
+    assert err <= tol, (what, err.item())
+
+
+# tokens, widths: sums over many tokens beside short ones, many tiles (taken as tickets), operands whose
+# rows are copied, long sums of few and of many tokens, every kind at sizes of a real block
+LARGE = [(16384, 128, 264, "bf16"), (8192, 132, 260, "f32"), (20000, 64, 5128, "bf16"), (4096, 1024, 4096, "bf16"),
+         (2600, 1032, 2600, "bf16"), (2600, 520, 2616, "bf16"), (40, 16384, 520, "bf16"), (7, 12288, 1024, "f32"),
+         (150, 8192, 2048, "bf16"), (150, 1024, 11008, "bf16"), (600, 9216, 520, "bf16"), (500, 4096, 516, "f32"),
+         (1000, 2048, 8192, "bf16")]
+
+
+@pytest.mark.parametrize("N,d,F,dt", LARGE)
+def test_large_shapes(cuda_lib, N, d, F, dt):
+    """Against plain products in float64 on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(N + d)
+    rand = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(DT[dt])  # noqa: E731
+    x, wg, wu, dh, b = rand(N, d), rand(F, d, std=d ** -0.5), rand(F, d, std=d ** -0.5), rand(N, F), rand(F)
+    X, G, U, D = (t.double().requires_grad_() for t in (x, wg, wu, b))
+    want = _act64(X @ G.t(), "silu") * (X @ U.t())
+    h, _ = api.lce_gated_forward(x, wg, wu)
+    _close(h, want.detach(), FWD[dt], "h")
+    grads = torch.autograd.grad((want * dh.double()).sum(), (X, G, U))
+    for name, a, w in zip(("dx", "dwg", "dwu"), api.lce_gated_backward(x, wg, wu, dh), grads):
+        _close(a, w, BWD[dt], name)
+    del want, grads
+    for act in ("gelu", "none"):
+        want = _act64(X @ G.t() + D, act)
+        y, _ = api.lce_linear_forward(x, wg, b, dh, activation=act)
+        _close(y, want.detach() + dh.double(), FWD[dt], "y")
+        grads = torch.autograd.grad((want * dh.double()).sum(), (X, G, D))
+        for name, a, w in zip(("dx", "dw", "db"), api.lce_linear_backward(x, wg, b, dh, activation=act), grads):
+            _close(a, w, BWD[dt], name)
+
+
+def test_past_32_bit_offsets(cuda_lib):
+    """Results of more than 2^31 elements: the first and last rows, and sums over all of them."""
+    N, d, F = 70_000, 64, 32_768
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).bfloat16()  # noqa: E731
+    x, wg, wu = rand(N, d), rand(F, d, std=0.125), rand(F, d, std=0.125)
+    rows = torch.tensor([0, 1, N // 2, N - 257, N - 2, N - 1], device="cuda")
+    cols = torch.tensor([0, 5, F // 2, F - 1], device="cuda")
+    out = torch.full((N, F), 3.0, dtype=torch.bfloat16, device="cuda")
+    api.lce_gated_forward(x, wg, wu, out=out)
+    X, G, U = x.double(), wg.double(), wu.double()
+    _close(out[rows], _act64(X[rows] @ G.t(), "silu") * (X[rows] @ U.t()), FWD["bf16"], "h")
+    dx, dwg, dwu, _ = api.lce_gated_backward(x, wg, wu, out)     # dH = H
+    o = out[rows].double()
+    z, u = X[rows] @ G.t(), X[rows] @ U.t()
+    s = torch.sigmoid(z)
+    _close(dx[rows], (o * u * (s + z * s * (1 - s))) @ G + (o * z * s) @ U, BWD["bf16"], "dx")
+    o = out[:, cols].double()
+    z, u = X @ G[cols].t(), X @ U[cols].t()
+    s = torch.sigmoid(z)
+    _close(dwg[cols], (o * u * (s + z * s * (1 - s))).t() @ X, BWD["bf16"], "dwg")
+    _close(dwu[cols], (o * z * s).t() @ X, BWD["bf16"], "dwu")
+    r = torch.full_like(out, 0.5)
+    api.lce_linear_forward(x, wg, None, r, out=r)                # in place, past 2^31
+    _close(r[rows], X[rows] @ G.t() + 0.5, FWD["bf16"], "y")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [6, 300])
 def test_row_strides_and_in_place_residual(cuda_lib, dt, N):

@@ -377,7 +377,8 @@ lce_status_t lce_set_tile_config(int32_t config);
  * of every CTA then gives up, lets copies in flight land, frees its tensor memory and returns;
  * the launch sets the workspace timeout bit, so lce_check_error reports LCE_ERR_TIMEOUT, and the
  * CUDA context stays usable.  The hook clears itself after that one launch.  No fault, trap or
- * endless loop is involved.  LCE_ERR_INVALID_ARG unless on is 0 or 1.
+ * endless loop is involved.  The tensor-core launches of the feed-forward operators count too and
+ * withhold all operands.  LCE_ERR_INVALID_ARG unless on is 0 or 1.
  */
 lce_status_t lce_test_inject_stall(int32_t on);
 

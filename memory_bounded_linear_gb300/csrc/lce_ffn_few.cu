@@ -61,6 +61,7 @@ struct Params {
   const __nv_bfloat16* R; int64_t ldr;
   __nv_bfloat16* Y; int64_t ldy;
   unsigned* err;
+  int withhold;  // test hook (lce_test_inject_stall): no operand is loaded
 };
 
 // One result: feature f of token t.
@@ -121,8 +122,8 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   if (warp == 0) {
     if (lane == 0) {
       Ring r{0, 0u};
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      bool ok = !p.withhold;
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
         const uint32_t full = ptx::smem_addr(&ctl->full[r.stage]);
         if (!wait_bar(ptx::smem_addr(&ctl->empty[r.stage]), r.ph ^ 1u, abort_flag, p.err)) {
           ok = false;
@@ -297,6 +298,8 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   p.R = static_cast<const __nv_bfloat16*>(g.R); p.ldr = g.ldr;
   p.Y = static_cast<__nv_bfloat16*>(g.C); p.ldy = g.ldc;
   p.err = err;
+  p.withhold = g_inject_stall;  // one launch only
+  g_inject_stall = 0;
   p.idesc = ptx::idesc_bf16_f32(BM, p.nt, false, false);
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>(W * p.nt)) p.tmem_cols *= 2;

@@ -133,6 +133,7 @@ struct KParams {
   unsigned* err;
   unsigned* sched;         // scheduler counters, or null: tiles are dealt out round-robin
   int clear_flags;         // the first CTA clears the error flags
+  int withhold;            // test hook (lce_test_inject_stall): no operand is loaded
 };
 
 struct FMaps {
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      bool ok = true;
+      bool ok = !p.withhold;
       Ring ring{0, 0u};
       Tickets tickets = role_tickets(rank != 0);
       TileQueue<true, Ctl>& tq = tickets.tq;
@@ -1122,6 +1123,8 @@ cudaError_t run(const FfnTc* jobs, int njobs, const Plan& plan, unsigned* header
     }
   }
   p.clear_flags = !state->flags;
+  p.withhold = g_inject_stall;  // one launch only
+  g_inject_stall = 0;
   state->flags = true;
   switch (mode) {
     case FFN_LINEAR:

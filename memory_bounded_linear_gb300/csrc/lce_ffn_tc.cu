@@ -302,19 +302,22 @@ __device__ __forceinline__ uint4 pack(const float* v) {
   return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
-// 32 columns of one thread's row: z (and u) in registers, D or R read from and the result written to
-// the thread's row of the box (chunks first, first + 1, ...).  For GATED_DGU z keeps dG in the box
-// and the dU values in z; for fp32 pre-activation gradients both stay in registers (z, u).
+// 16 columns of one thread's row: z (and u) in registers, D or R read from and the result written to
+// the thread's row of the box (chunks first, first + 1, ...).  GATED_DGU: dU goes to the same place of
+// the row at row2.  fp32 pre-activation gradients stay in registers: dZ or dG in z, dU in u.
+// (16 columns and a loop around them, not a whole box unrolled: the fp32 GELU gradient of 32 columns
+// was 70 KB of code, and a short launch spent most of its time fetching it.)
 template <int MODE, int ACT, bool F32>
-__device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint32_t row, uint32_t sw,
-                                           int first, int col, int c_cols, const void* bias) {
+__device__ __forceinline__ void epilogue16(float (&z)[16], float (&u)[16], uint32_t row, uint32_t row2,
+                                           uint32_t sw, int first, int col, int c_cols,
+                                           const void* bias) {
   constexpr int CH = CHUNK<F32>;
   constexpr bool LINEAR = MODE == FFN_LINEAR || MODE == FFN_LINEAR_RES;
   constexpr bool DZ = Cfg<MODE>::DZ;
 #pragma unroll
-  for (int q = 0; q < 32 / CH; ++q) {
-    const uint32_t addr = row + ((static_cast<uint32_t>(first + q) ^ sw) << 4);
-    float d[CH], o[CH], b[CH];
+  for (int q = 0; q < 16 / CH; ++q) {
+    const uint32_t place = (static_cast<uint32_t>(first + q) ^ sw) << 4;
+    float d[CH], o[CH], b[CH], du[CH];
     if (LINEAR || MODE == FFN_LINEAR_DZ) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) b[i] = 0.f;
@@ -324,7 +327,7 @@ __device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint3
         unpack<F32>(__ldg(reinterpret_cast<const uint4*>(pb)), b);
       }
     }
-    if (Cfg<MODE>::LOADS) unpack<F32>(ptx::ld_shared_v4(addr), d);
+    if (Cfg<MODE>::LOADS) unpack<F32>(ptx::ld_shared_v4(row + place), d);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const float v = z[q * CH + i];
@@ -340,54 +343,50 @@ __device__ __forceinline__ void epilogue32(float (&z)[32], float (&u)[32], uint3
         act_grad<ACT, !F32>(MODE == FFN_LINEAR_DZ ? v + b[i] : v, a, g);
         if constexpr (MODE == FFN_GATED_DGU) {
           o[i] = d[i] * u[q * CH + i] * g;
-          if (F32) { z[q * CH + i] = o[i]; u[q * CH + i] = d[i] * a; }
-          else z[q * CH + i] = d[i] * a;
+          du[i] = d[i] * a;
         } else {
           o[i] = d[i] * g;
-          if (F32) z[q * CH + i] = o[i];
+        }
+        if (F32) {
+          z[q * CH + i] = o[i];
+          if (MODE == FFN_GATED_DGU) u[q * CH + i] = du[i];
         }
       }
     }
-    if (!(F32 && DZ)) {
-      const uint4 w = pack<F32>(o);
-      ptx::st_shared_v4(addr, w.x, w.y, w.z, w.w);
+    if constexpr (!(F32 && DZ)) {
+      uint4 w = pack<F32>(o);
+      ptx::st_shared_v4(row + place, w.x, w.y, w.z, w.w);
+      if constexpr (MODE == FFN_GATED_DGU) {
+        w = pack<F32>(du);
+        ptx::st_shared_v4(row2 + place, w.x, w.y, w.z, w.w);
+      }
     }
   }
 }
 
-// 32 columns of a warp's 32 rows, fp32 values of one row per thread, as three bf16 parts: through
-// `stage` (2 KB of shared memory, 64-byte rows with their 16-byte chunks rotated against bank
-// conflicts), so that four lanes write a row's 64 bytes together.  rows, cols: what exists of the box;
-// the padding of a row to a multiple of 8 columns may be written, nothing reads it.
-__device__ __forceinline__ void store_parts(const float (&v)[32], uint32_t stage, __nv_bfloat16* out,
-                                            int64_t ld, int64_t stride, int64_t rows, int cols) {
-  const int lane = threadIdx.x & 31;
-  uint32_t w[3][16];
+// 16 fp32 values of a row as three bf16 parts: 32 bytes (a sector) of each part's row.  cols: what
+// exists from here on; the padding of a row to a multiple of 8 columns may be written, nothing reads
+// it.
+__device__ __forceinline__ void store_parts(const float (&v)[16], __nv_bfloat16* out, int64_t stride,
+                                            int cols) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float a[3], b[3];
-    split_bf16(v[2 * i], a);
-    split_bf16(v[2 * i + 1], b);
-#pragma unroll
-    for (int s = 0; s < 3; ++s) w[s][i] = pack2(a[s], b[s]);
-  }
-#pragma unroll
-  for (int s = 0; s < 3; ++s) {
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      ptx::st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[s][4 * c], w[s][4 * c + 1],
-                        w[s][4 * c + 2], w[s][4 * c + 3]);
-    __syncwarp();
-    const int c = lane & 3;
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      const uint4 x = ptx::ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-      if (r < rows && c * 8 < cols) *reinterpret_cast<uint4*>(out + s * stride + r * ld + c * 8) = x;
+      float a[3], b[3];
+      split_bf16(v[q * 8 + 2 * i], a);
+      split_bf16(v[q * 8 + 2 * i + 1], b);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) w[s][i] = pack2(a[s], b[s]);
+    }
+    if (q * 8 < cols) {
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+        *reinterpret_cast<uint4*>(out + s * stride + q * 8) =
+            make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
     }
   }
-  __syncwarp();
 }
 
 // Tickets of one role: from the queue, or where no counters are used dealt out round-robin, which every
@@ -478,6 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t my_boxes = boxes + e * nboxes * STAGE_BUF_BYTES;
   const uint32_t sw = lane & 7;
   uint32_t in_flight = 0;              // boxes being loaded, a bit each
+  int turn = 0;                        // boxes stored so far, modes that load none
   int split_tile = -1;                 // SPLIT: the cluster whose tile is finished together
   // R or D of one box of results into box i, once the stores from the boxes have been read: eight lanes
   // copy a row's 128 bytes; zeros outside the result.
@@ -497,70 +497,52 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::copy_commit();
     in_flight |= 1u << i;
   };
-  // One box of results through box i: columns col .., rows box_row .. + 31.  load(h, z, u) gives 32
-  // accumulator columns of the thread's row; loaded() is called once all have been read.
-  auto process = [&](int i, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load,
+  // One box of results through box `slot` (modes that load none: through the boxes in turn, whatever
+  // the tile): columns col .., rows box_row .. + 31.  load(c, z, u) gives 16
+  // accumulator columns of the thread's row from the box's column c on; loaded() is called once all
+  // have been read.
+  auto process = [&](int slot, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load,
                      auto&& loaded) {
+    const int i = Cf::LOADS ? slot : turn++ & (nboxes - 1);
     const uint32_t box = my_boxes + i * STAGE_BUF_BYTES, row_addr = box + lane * 128;
+    // dU leaves through the other box: a bf16 tile has one box of D per warp
+    const uint32_t box2 = my_boxes + (i ^ 1) * STAGE_BUF_BYTES, row2 = box2 + lane * 128;
     if (Cf::LOADS) {
       // the other box, if it is being loaded, was asked for later
       in_flight &= ~(1u << i);
       if (in_flight) ptx::copy_wait<1>();
       else ptx::copy_wait<0>();
-      __syncwarp();
-    } else {
-      if (lane == 0) {  // the box's last store has been read
-        if (nboxes == 2) ptx::bulk_wait_read<1>();
-        else ptx::bulk_wait_read<0>();
-      }
-      __syncwarp();
+    } else if (lane == 0) {  // the box's last store, the one before the latest if there are two, is read
+      if (nboxes == 2) ptx::bulk_wait_read<1>();
+      else ptx::bulk_wait_read<0>();
     }
-    [[maybe_unused]] uint32_t keep[MODE == FFN_GATED_DGU && !F32 ? 32 : 1];
-#pragma unroll
-    for (int h = 0; h < UC / 32; ++h) {
-      float z[32], u[32];
-      load(h, z, u);
-      if (h == UC / 32 - 1) loaded();
-      if constexpr (MODE == FFN_GRADS)
-        epilogue32<MODE, LCE_ACT_NONE, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols, nullptr);
-      else
-        dispatch_act(p.act, [&](auto tag) {
-          epilogue32<MODE, decltype(tag)::value, F32>(z, u, row_addr, sw, h * 4, col + h * 32, c_cols,
-                                                      p.bias);
-        });
-      if constexpr (MODE == FFN_GATED_DGU && !F32) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) keep[h * 16 + k] = pack2(z[2 * k], z[2 * k + 1]);
+    __syncwarp();
+    auto columns = [&](auto tag) {
+#pragma unroll 1
+      for (int c = 0; c < UC; c += 16) {
+        float z[16], u[16];
+        load(c, z, u);
+        if (c + 16 == UC) loaded();
+        epilogue16<MODE, decltype(tag)::value, F32>(z, u, row_addr, row2, sw, c / CHUNK<F32>, col + c,
+                                                    c_cols, p.bias);
+        if constexpr (DZ && F32) {
+          if (box_row + lane < p.m_rows) {
+            const int64_t off = (box_row + lane) * p.part_ld + col + c;
+            store_parts(z, p.parts[0] + off, p.part_stride, c_cols - col - c);
+            if (GATED) store_parts(u, p.parts[1] + off, p.part_stride, c_cols - col - c);
+          }
+        }
       }
-      if constexpr (DZ && F32) {
-        // the box has been read: it stages the parts
-        const int64_t off = box_row * p.part_ld + col;
-        store_parts(z, box, p.parts[0] + off, p.part_ld, p.part_stride, p.m_rows - box_row, c_cols - col);
-        if (GATED)
-          store_parts(u, box, p.parts[1] + off, p.part_ld, p.part_stride, p.m_rows - box_row,
-                      c_cols - col);
-      }
-    }
+    };
+    if constexpr (MODE == FFN_GRADS) columns(ActTag<LCE_ACT_NONE>{});
+    else dispatch_act(p.act, columns);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if constexpr (!(DZ && F32)) {
       if (lane == 0) {
         ptx::tma_store_2d(mC, box, col, box_row);
+        if (MODE == FFN_GATED_DGU) ptx::tma_store_2d(&maps.c2, box2, col, box_row);
         ptx::bulk_commit();
-      }
-      if constexpr (MODE == FFN_GATED_DGU) {
-        // dU through the other box: a bf16 tile has one box of D per warp
-        const uint32_t row2 = my_boxes + (i ^ 1) * STAGE_BUF_BYTES + lane * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          ptx::st_shared_v4(row2 + ((static_cast<uint32_t>(c) ^ sw) << 4), keep[4 * c], keep[4 * c + 1],
-                            keep[4 * c + 2], keep[4 * c + 3]);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::tma_store_2d(&maps.c2, my_boxes + (i ^ 1) * STAGE_BUF_BYTES, col, box_row);
-          ptx::bulk_commit();
-        }
       }
     }
   };
@@ -781,9 +763,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (col >= col_end) break;  // same for every thread of the warp
           const int at = (half * per_half + un) * UC;  // accumulator column
           process(un & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
-                  [&](int h, float (&z)[32], float (&u)[32]) {
-                    ptx::tmem_load32(tbase + at + h * 32, z);
-                    if (GATED) ptx::tmem_load32(tbase + p.bn / 2 + at + h * 32, u);
+                  [&](int c, float (&z)[16], float (&u)[16]) {
+                    ptx::tmem_load16(tbase + at + c, z);
+                    if (GATED) ptx::tmem_load16(tbase + p.bn / 2 + at + c, u);
                   },
                   [&] { if (col + UC >= col_end) release(); });
           if (Cf::LOADS && col + nboxes * UC < col_end)
@@ -802,31 +784,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int steps = steps_per_pair<F32>(jb.nkb) * jb.pairs;
       const int box_row = tp.tm * TILE + static_cast<int>(rank) * BM + q * 32;
       const int col_end = min(jb.c_cols, (tp.tn + 1) * cols);
-      // 32 columns from all pairs, in the order of the pieces
-      auto gather = [&](int c, float (&v)[32]) {
+      // 16 columns from all pairs, in the order of the pieces
+      auto gather = [&](int c, float (&v)[16]) {
         const uint32_t at = base + ((c >> 2) * BM + q * 32 + lane) * 16;
+        float4 t[MAX_SPLIT][4];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float4 t[MAX_SPLIT][4];
+        for (int s = 0; s < MAX_SPLIT; ++s) {
+          const Range r = piece_of(steps, s, split);
+          const bool some = s < split && r.lo < r.hi;
+          const uint32_t peer = ptx::mapa_shared(at, some ? 2 * s + rank : crank);
 #pragma unroll
-          for (int s = 0; s < MAX_SPLIT; ++s) {
-            const Range r = piece_of(steps, s, split);
-            const bool some = s < split && r.lo < r.hi;
-            const uint32_t peer = ptx::mapa_shared(at + g * 4 * BM * 16, some ? 2 * s + rank : crank);
+          for (int i = 0; i < 4; ++i)
+            t[s][i] = some ? ptx::ld_shared_cluster_v4(peer + i * BM * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              t[s][i] = some ? ptx::ld_shared_cluster_v4(peer + i * BM * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 4; ++i) {
+          float4 x = t[0][i];
+#pragma unroll
+          for (int s = 1; s < MAX_SPLIT; ++s) {
+            x.x += t[s][i].x; x.y += t[s][i].y; x.z += t[s][i].z; x.w += t[s][i].w;
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 x = t[0][i];
-#pragma unroll
-            for (int s = 1; s < MAX_SPLIT; ++s) {
-              x.x += t[s][i].x; x.y += t[s][i].y; x.z += t[s][i].z; x.w += t[s][i].w;
-            }
-            v[g * 16 + 4 * i] = x.x; v[g * 16 + 4 * i + 1] = x.y;
-            v[g * 16 + 4 * i + 2] = x.z; v[g * 16 + 4 * i + 3] = x.w;
-          }
+          v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
         }
       };
 #pragma unroll 1
@@ -835,9 +813,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int col = tp.tn * cols + b * UC;
         if (col >= col_end) break;
         process(n & (nboxes - 1), &maps.c[tp.job], jb.c_cols, col, box_row,
-                [&](int h, float (&z)[32], float (&u)[32]) {
-                  gather(b * UC + h * 32, z);
-                  if (GATED) gather(p.bn / 2 + b * UC + h * 32, u);
+                [&](int c, float (&z)[16], float (&u)[16]) {
+                  gather(b * UC + c, z);
+                  if (GATED) gather(p.bn / 2 + b * UC + c, u);
                 },
                 [] {});
         const int next = col + nboxes * 2 * split * UC;

@@ -170,6 +170,23 @@ def test_large_shapes(cuda_lib, N, d, F, dt):
             _close(a, w, BWD[dt], name)
 
 
+@pytest.mark.parametrize("N,d,F", [(150, 128, 20_000), (150, 1024, 11_008), (100, 136, 30_000), (700, 8, 40_000)])
+def test_short_sums_store_every_tile(cuda_lib, N, d, F):
+    """Weight gradients of few tokens: many tiles of short sums whose results leave as fast as the
+    boxes they leave through come free; a box written too early shows as wrong values in some of
+    many rounds."""
+    x, dy = _rand(1, "bf16", N, d).cuda(), _rand(2, "bf16", N, F).cuda()
+    w = _rand(3, "bf16", F, d, std=d ** -0.5).cuda()
+    want = dy.double().t() @ x.double()
+    first = None
+    for _ in range(20):
+        dw = api.lce_linear_backward(x, w, None, dy, parts="dw")[1]
+        if first is None:
+            first = dw
+            assert ((dw.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3 * N ** 0.5).all()
+        assert torch.equal(dw, first)
+
+
 def test_past_32_bit_offsets(cuda_lib):
     """Results of more than 2^31 elements: the first and last rows, and sums over all of them."""
     N, d, F = 70_000, 64, 32_768

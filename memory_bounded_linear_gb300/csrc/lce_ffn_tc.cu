@@ -364,28 +364,37 @@ __device__ __forceinline__ void epilogue16(float (&z)[16], float (&u)[16], uint3
   }
 }
 
-// 16 fp32 values of a row as three bf16 parts: 32 bytes (a sector) of each part's row.  cols: what
-// exists from here on; the padding of a row to a multiple of 8 columns may be written, nothing reads
-// it.
-__device__ __forceinline__ void store_parts(const float (&v)[16], __nv_bfloat16* out, int64_t stride,
-                                            int cols) {
+// 16 columns of a warp's 32 rows, fp32 values of one row per thread, as three bf16 parts.  Lanes
+// exchange halves in pairs, so that two lanes write the 32 bytes (a sector) of one row of a part
+// together.  out: the box's first row, at these columns; rows, cols: what exists from there on.  The
+// padding of a row to a multiple of 8 columns may be written, nothing reads it.
+__device__ __forceinline__ void store_parts(const float (&v)[16], __nv_bfloat16* out, int64_t ld,
+                                            int64_t stride, int64_t rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1;
+  uint32_t w[3][8];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t w[3][4];
+  for (int i = 0; i < 8; ++i) {
+    float a[3], b[3];
+    split_bf16(v[2 * i], a);
+    split_bf16(v[2 * i + 1], b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a[3], b[3];
-      split_bf16(v[q * 8 + 2 * i], a);
-      split_bf16(v[q * 8 + 2 * i + 1], b);
+    for (int s = 0; s < 3; ++s) w[s][i] = pack2(a[s], b[s]);
+  }
+  const int row = lane & ~1, c = odd ? 8 : 0;  // rows row and row + 1; this lane writes columns c ..
 #pragma unroll
-      for (int s = 0; s < 3; ++s) w[s][i] = pack2(a[s], b[s]);
-    }
-    if (q * 8 < cols) {
+  for (int s = 0; s < 3; ++s) {
+    uint32_t got[4];
 #pragma unroll
-      for (int s = 0; s < 3; ++s)
-        *reinterpret_cast<uint4*>(out + s * stride + q * 8) =
-            make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
-    }
+    for (int i = 0; i < 4; ++i)
+      got[i] = __shfl_xor_sync(0xffffffffu, odd ? w[s][i] : w[s][4 + i], 1);
+    const uint4 even_row = odd ? make_uint4(got[0], got[1], got[2], got[3])
+                               : make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+    const uint4 odd_row = odd ? make_uint4(w[s][4], w[s][5], w[s][6], w[s][7])
+                              : make_uint4(got[0], got[1], got[2], got[3]);
+    __nv_bfloat16* o = out + s * stride + row * ld + c;
+    if (c < cols && row < rows) *reinterpret_cast<uint4*>(o) = even_row;
+    if (c < cols && row + 1 < rows) *reinterpret_cast<uint4*>(o + ld) = odd_row;
   }
 }
 
@@ -526,11 +535,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         epilogue16<MODE, decltype(tag)::value, F32>(z, u, row_addr, row2, sw, c / CHUNK<F32>, col + c,
                                                     c_cols, p.bias);
         if constexpr (DZ && F32) {
-          if (box_row + lane < p.m_rows) {
-            const int64_t off = (box_row + lane) * p.part_ld + col + c;
-            store_parts(z, p.parts[0] + off, p.part_stride, c_cols - col - c);
-            if (GATED) store_parts(u, p.parts[1] + off, p.part_stride, c_cols - col - c);
-          }
+          const int64_t off = box_row * p.part_ld + col + c, rows = p.m_rows - box_row;
+          store_parts(z, p.parts[0] + off, p.part_ld, p.part_stride, rows, c_cols - col - c);
+          if (GATED)
+            store_parts(u, p.parts[1] + off, p.part_ld, p.part_stride, rows, c_cols - col - c);
         }
       }
     };

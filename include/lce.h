@@ -255,7 +255,8 @@ lce_status_t lce_forward_static_scratch(const void* H, const void* W, const int6
  *     not depend on the other rows' values, but its summation order may differ between the call
  *     for a few tokens and the call for many.
  *   - An inf or NaN in an operand makes the outputs it takes part in inf or NaN.  With LCE_F32 an
- *     inf may come out as NaN: operands are summed in parts.
+ *     inf may come out as NaN: operands are summed in parts.  Where a ReLU is 0 the gradient before it
+ *     is 0 whatever the outgoing one holds.
  */
 typedef enum {
   LCE_ACT_NONE = 0,

@@ -65,7 +65,7 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ void act_grad(float x, float& a, float& d) {
   if constexpr (ACT == LCE_ACT_RELU) {
     a = x > 0.f ? x : (x == x ? 0.f : x);
-    d = x > 0.f ? 1.f : 0.f;
+    d = x <= 0.f ? 0.f : 1.f;
   } else if constexpr (ACT == LCE_ACT_SILU) {
     const float s = sigmoid<FAST>(x);
     a = x * s;
@@ -91,6 +91,12 @@ __device__ __forceinline__ void act_grad(float x, float& a, float& d) {
     a = x;
     d = 1.f;
   }
+}
+
+// g act'(x) for act'(x) = d: what the ReLU masks is 0 also where g is an infinity or NaN.
+template <int ACT>
+__device__ __forceinline__ float chain(float g, float d) {
+  return ACT == LCE_ACT_RELU ? (d != 0.f ? g : 0.f) : g * d;
 }
 
 // Calls f(integral_constant<int, activation>) for a run-time activation.

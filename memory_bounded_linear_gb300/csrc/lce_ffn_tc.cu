@@ -342,10 +342,10 @@ __device__ __forceinline__ void epilogue16(float (&z)[16], float (&u)[16], uint3
         float a, g;
         act_grad<ACT, !F32>(MODE == FFN_LINEAR_DZ ? v + b[i] : v, a, g);
         if constexpr (MODE == FFN_GATED_DGU) {
-          o[i] = d[i] * u[q * CH + i] * g;
+          o[i] = chain<ACT>(d[i] * u[q * CH + i], g);
           du[i] = d[i] * a;
         } else {
-          o[i] = d[i] * g;
+          o[i] = chain<ACT>(d[i], g);
         }
         if (F32) {
           z[q * CH + i] = o[i];

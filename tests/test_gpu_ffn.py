@@ -314,6 +314,25 @@ def test_rows_do_not_mix(cuda_lib, dt, N):
         assert torch.equal(got[:, cols], clean[k][:, cols])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_relu_masks_what_is_not_finite(cuda_lib, dt):
+    """An inf or NaN of the outgoing gradient where the ReLU is 0 does not reach the gradients."""
+    N, d, out = 70, 72, 136
+    x = torch.ones(N, d, dtype=DT[dt])
+    w = _rand(1, dt, out, d).abs()
+    w[::3] *= -1                                     # every third output is below zero in all rows
+    wu, dy = _rand(2, dt, out, d, std=d ** -0.5), _rand(3, dt, N, out)
+    bad = dy.clone()
+    bad[0, 0], bad[5, 3], bad[69, 135] = float("nan"), float("inf"), float("-inf")
+    args = x.cuda(), w.cuda()
+    for clean, got in zip(api.lce_linear_backward(*args, None, dy.cuda(), activation="relu")[:2],
+                          api.lce_linear_backward(*args, None, bad.cuda(), activation="relu")[:2]):
+        assert torch.isfinite(got).all() and torch.equal(got, clean)
+    clean = api.lce_gated_backward(*args, wu.cuda(), dy.cuda(), activation="relu")[1]
+    got = api.lce_gated_backward(*args, wu.cuda(), bad.cuda(), activation="relu")[1]
+    assert torch.isfinite(got).all() and torch.equal(got, clean)
+
+
 def test_large_magnitudes_of_the_activations(cuda_lib):
     """Pre-activations far outside the exponential's range: results stay finite and exact limits."""
     z = torch.tensor([-3e38, -1e30, -200.0, -90.0, -88.0, 0.0, 88.0, 90.0, 200.0, 1e30], dtype=torch.float32)

@@ -329,27 +329,33 @@ __device__ __forceinline__ void epilogue16(float (&z)[16], float (&u)[16], uint3
     }
     if (Cfg<MODE>::LOADS) unpack<F32>(ptx::ld_shared_v4(row + place), d);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float v = z[q * CH + i];
+    for (int i = 0; i < CH; i += 2) {
+      auto two = [](float* x) { return make_float2(x[0], x[1]); };
+      auto put = [](float* x, float2 v) { x[0] = v.x; x[1] = v.y; };
+      float2 v = two(z + q * CH + i);
       if constexpr (MODE == FFN_GRADS) {
-        o[i] = v;
+        put(o + i, v);
       } else if constexpr (LINEAR) {
-        o[i] = act<ACT, !F32>(v + b[i]);
-        if (MODE == FFN_LINEAR_RES) o[i] += d[i];
+        v = act<ACT, !F32>(vadd(v, two(b + i)));
+        if (MODE == FFN_LINEAR_RES) v = vadd(v, two(d + i));
+        put(o + i, v);
       } else if constexpr (MODE == FFN_GATED) {
-        o[i] = act<ACT, !F32>(v) * u[q * CH + i];
+        put(o + i, vmul(act<ACT, !F32>(v), two(u + q * CH + i)));
       } else {
-        float a, g;
-        act_grad<ACT, !F32>(MODE == FFN_LINEAR_DZ ? v + b[i] : v, a, g);
+        float2 a, g;
+        if (MODE == FFN_LINEAR_DZ) v = vadd(v, two(b + i));
+        act_grad<ACT, !F32>(v, a, g);
+        float2 r = two(d + i);
         if constexpr (MODE == FFN_GATED_DGU) {
-          o[i] = chain<ACT>(d[i] * u[q * CH + i], g);
-          du[i] = d[i] * a;
-        } else {
-          o[i] = chain<ACT>(d[i], g);
+          a = vmul(r, a);
+          r = vmul(r, two(u + q * CH + i));
+          put(du + i, a);
         }
+        r = chain<ACT>(r, g);
+        put(o + i, r);
         if (F32) {
-          z[q * CH + i] = o[i];
-          if (MODE == FFN_GATED_DGU) u[q * CH + i] = du[i];
+          put(z + q * CH + i, r);
+          if (MODE == FFN_GATED_DGU) put(u + q * CH + i, a);
         }
       }
     }

@@ -27,18 +27,23 @@
 // steps of F32_STEP k-blocks, each into a fresh accumulator, which the epilogue warps add up in
 // registers (4e-7 there, for a drain of about 1,000 cycles per 12,000 of products).
 //
-// With few tiles (SPLIT) a cluster of 2 or 4 pairs computes each: every pair sums a piece of the K loop,
-// puts its partial sums into its ring's memory, and finishes some of the tile's boxes from all of
-// them, read through distributed shared memory in the order of the pieces.
+// With few tiles (SPLIT) a cluster of 2 or 4 pairs computes each: every pair sums a piece of the K
+// loop, puts its partial sums into its ring's memory, and finishes some of the tile's boxes from all
+// of them, read through distributed shared memory in the order of the pieces.
 //
 // The outgoing gradient D and the residual R enter, and C leaves, through 4 KB boxes of the epilogue
-// warps (32 rows x 128 bytes, 128-byte swizzle): 16-byte copies by the warp's lanes, each thread rewrites
-// its own row, TMA store.  (Boxes loaded by TMA held up the operands behind them in its queue: tiles
-// of 4096 x 2048 -> 8192 took 22,000 cycles instead of 17,000.)  Modes that load boxes have two per warp, both fetched while the products of their tile
-// run, and a ring of five 32 KB stages; so have the others while K is short, where the epilogue decides
-// (a warp then fills one box while the other leaves); with long K they have one box and six stages.
+// warps (32 rows x 128 bytes, 128-byte swizzle): 16-byte copies by the warp's lanes, each thread
+// rewrites its own row, TMA store.  (Boxes loaded by TMA held up the operands behind them in its
+// queue: tiles of 4096 x 2048 -> 8192 took 22,000 cycles instead of 17,000.)  Modes that load boxes
+// have two per warp, both fetched while the products of their tile run, and a ring of five 32 KB
+// stages; so have the others while K is short, where the epilogue decides (a warp then fills one box
+// while the other leaves); with long K they have one box and six stages.
 //
-// Bound: tensor pipe for many tokens.  Ragged edges: TMA zero-fills loads and clips stores.
+// Bound: tensor pipe for many tokens (products hide the epilogue from K = 1024 on; at K = 512 a tile's
+// epilogue takes 11,000 cycles, its products 4,100).  Measured: gated backward 16384 x 4096 -> 16384
+// 7.1 ms (1,860 TFLOP/s), linear 4096 x 8192 -> 2048 84 us (1,630: 128 tiles on 76 pairs), gated forward
+// 777 x 4096 -> 10952 97 us (1,430: four row tiles for 3.04).
+// Ragged edges: TMA zero-fills loads and clips stores.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -75,8 +80,8 @@ struct Cfg {
   static constexpr bool LOADS = DZ || MODE == FFN_LINEAR_RES;  // boxes of D or R are loaded
 };
 
-// Shared memory: the stages of the ring, then the boxes of the eight epilogue warps: six stages and one
-// box per warp, or five and two.
+// Shared memory: the stages of the ring, then the boxes of the eight epilogue warps: six stages and
+// one box per warp, or five and two.
 constexpr int RING_AND_BOXES = 6 * STAGE_BYTES + EPI_WARPS * STAGE_BUF_BYTES;
 constexpr int SMEM_BYTES = RING_AND_BOXES + 1024 + CTL_BYTES;
 static_assert(5 * STAGE_BYTES + 2 * EPI_WARPS * STAGE_BUF_BYTES == RING_AND_BOXES, "one size");
@@ -513,9 +518,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     in_flight |= 1u << i;
   };
   // One box of results through box `slot` (modes that load none: through the boxes in turn, whatever
-  // the tile): columns col .., rows box_row .. + 31.  load(c, z, u) gives 16
-  // accumulator columns of the thread's row from the box's column c on; loaded() is called once all
-  // have been read.
+  // the tile): columns col .., rows box_row .. + 31.  load(c, z, u) gives 16 accumulator columns of the
+  // thread's row from the box's column c on; loaded() is called once all have been read.
   auto process = [&](int slot, const CUtensorMap* mC, int c_cols, int col, int box_row, auto&& load,
                      auto&& loaded) {
     const int i = Cf::LOADS ? slot : turn++ & (nboxes - 1);
@@ -603,21 +607,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           // CTA 0 loads its columns' rows of Wg, CTA 1 the same rows of Wu
           ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], &maps.b[0][rank], m0,
                                                tp.tn * (p.bn / 2), base, ctl, ring, abort_flag, p.err,
-                                               rank, leader, p.bn,
-                                                 stages);
+                                               rank, leader, p.bn, stages);
         } else {
           const int n0 = tp.tn * p.bn + static_cast<int>(rank) * (p.bn / 2);
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
               ok = produce_tile<true, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                  maps.b[tp.job], m0, n0, base, ctl, ring, abort_flag,
-                                                 p.err, rank, leader, p.bn,
-                                                 stages);
+                                                 p.err, rank, leader, p.bn, stages);
             else
               ok = produce_tile<false, true, F32>(jb.nkb, jb.pairs, range, maps.a[tp.job],
                                                   maps.b[tp.job], m0, n0, base, ctl, ring,
-                                                  abort_flag, p.err, rank, leader, p.bn,
-                                                 stages);
+                                                  abort_flag, p.err, rank, leader, p.bn, stages);
           } else {
             ok = produce_tile<false, false, F32>(jb.nkb, 1, range, maps.a[0], maps.b[0], m0, n0, base,
                                                  ctl, ring, abort_flag, p.err, rank, leader, p.bn,
@@ -662,14 +663,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t d_tmem = tmem_base + acc * TILE;
           if constexpr (MODE == FFN_GRADS) {
             if (jb.mn)
-              ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
-                                       stages);
+              ok = mma_tile<true, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask,
+                                        p.bn, stages);
             else
-              ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
-                                       stages);
+              ok = mma_tile<false, true>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask,
+                                         p.bn, stages);
           } else {
-            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask, p.bn,
-                                       stages);
+            ok = mma_tile<false, false>(blocks, d_tmem, base, ctl, ring, abort_flag, p.err, pair_mask,
+                                        p.bn, stages);
           }
           if (!ok) break;
           ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[acc]), pair_mask);

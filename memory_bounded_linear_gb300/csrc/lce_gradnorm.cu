@@ -154,11 +154,13 @@ __device__ __forceinline__ void visit(const Chunk& c, const uint4 (&q)[UNROLL], 
 template <bool INF, int CAP>
 __global__ void __launch_bounds__(THREADS, 2)
     norm_kernel(const __grid_constant__ Table<CAP> t, double* part) {
+  int64_t i = blockIdx.x;  // the grid is not larger than the number of chunks
+  Chunk c = chunk_of(t, i);
   ptx::wait_for_previous();  // no memory of the caller is touched before this
+  ptx::launch_dependents();  // its blocks take the places of this grid's as they end
   double sum = 0.0;
   unsigned m = 0;
-  for (int64_t i = blockIdx.x; i < t.first[t.count]; i += gridDim.x) {
-    const Chunk c = chunk_of(t, i);
+  while (true) {
     uint4 q[UNROLL];
     load<false>(c, q);
     Acc a{0.f, 0u};
@@ -166,8 +168,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     else visit<__nv_bfloat16, INF>(c, q, a);
     sum += static_cast<double>(a.s);
     m = max(m, a.m);
+    i += gridDim.x;
+    if (i >= t.first[t.count]) break;
+    c = chunk_of(t, i);
   }
-  ptx::launch_dependents();
   const double r = reduce<INF>(INF ? static_cast<double>(m) : sum);
   if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
@@ -242,6 +246,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint4 q[UNROLL];
   load<true>(c, q);
   ptx::wait_for_previous();
+  ptx::launch_dependents();
   const float v = total_of<INF>(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *total = v;
   const float r = max_norm / (v + 1e-6f);

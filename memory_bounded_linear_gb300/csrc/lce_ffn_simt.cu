@@ -56,15 +56,26 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
     }
   }
   ptx::launch_dependents();
+  // The lanes' sums: at each step a lane keeps half of its values and adds the other lane's to them, so
+  // that the last one ends with value lane / (32 / V), in 31 shuffles for 32 values instead of 160.
+  constexpr int V = R * NT;
+  float s[V];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int i = 0; i < V; ++i) s[i] = acc[i / NT][i % NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float v = acc[r][t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) sh[warp][r * NT + t] = v;
+  for (int o = 16, n = V / 2; o > 0; o >>= 1, n >>= 1) {
+    if (n == 0) {
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+      continue;
     }
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? s[i] : s[i + n], o);
+      s[i] = (upper ? s[i + n] : s[i]) + other;
+    }
+  }
+  if (lane % (32 / V) == 0) sh[warp][lane / (32 / V)] = s[0];
   __syncthreads();
   const int i = threadIdx.x;  // one result per thread
   if (i >= ROWS * NT) return;

@@ -41,9 +41,14 @@ bool sizes_ok(int64_t N, int64_t d, int64_t width, lce_dtype_t dt) {
 //   gated 128 x 4096 x 11008 40 / 47, 160: 42 / 47, 192: 49 / 48 (a tile for each of more than half the
 //     SMs, no joining); 48 x 4096 x 8192 27 / 27, 96: 32 / 27 (two sums to join per tile);
 //     96 x 2048 x 1024 8.7 / 11.9, 128: 22 / 12 (its partial sums no longer fit)
-//   fp32 linear 16 x 2048 -> 8192 51 / 63, 33: 115 / 64 (the weights are read again for every 8 tokens)
+//   fp32 linear 32 x 2048 -> 8192 49 / 67, 64: 83 / 67, 40 x 4096 -> 4096 69 / 80; small products, for
+//     which the tiles take about 12 us + 6 per 1000 of d: 64 x 512 -> 1024 4.5 / 14, 256: 14.9 / 14.5,
+//     100 x 1024 -> 1024 12.6 / 16.5, 500 x 256 -> 512 10.0 / 12.2, 1000: 17.4 / 12.4, 100 x 6000 -> 512
+//     31 / 48; a result costs about as much as 100 more of d (4096 x 128 -> 144 15.9 / 10.0)
 bool few_tokens(int64_t N, int64_t d, int64_t width, int weights, lce_dtype_t dt) {
-  if (dt == LCE_F32) return N <= 16;
+  if (dt == LCE_F32)
+    return N <= 48 ||
+           (N <= 4096 && static_cast<double>(N) * width * weights * (d + 100) <= 1e8 + 5.6e4 * d);
   if (N <= 32) return true;
   if (weights == 1) return N <= 128 || (N <= FFN_FEW_TOKENS && d >= 2 * width);
   const int64_t tiles = (width + 127) / 128;  // of the stream: feature rows of one CTA

@@ -14,14 +14,15 @@ namespace lce {
 namespace {
 
 // ---------------------------------------------------------------- fp32 products of a few tokens
-// Bound by reading the weights once (HBM).  A block computes ROWS features (4; gated 2 of Wg and 2 of
-// Wu) for NT tokens; its eight warps take 512-byte pieces of K in turn, lanes four elements each,
-// and each weight vector loaded serves NT tokens from registers (X comes from L1/L2).  The lanes'
-// sums meet by shuffles, the warps' in shared memory, in a fixed order.  2 x 2048 -> 2048 with GELU takes
-// 5.7 us (2.9 TB/s; most of it the launch and the latency of the first loads).
+// Bound by reading the weights once (HBM), from about eight tokens on by the products.  A warp computes
+// ROWS features (4; gated 2 of Wg and 2 of Wu) for NT tokens, or WAYS warps of a block together: they
+// take 512-byte pieces of K in turn, lanes four elements each, and each weight vector loaded serves NT
+// tokens from registers (X comes from L1/L2).  The lanes' sums meet by shuffles, the warps' in shared
+// memory, in a fixed order.  1 x 2048 -> 8192 takes 12.3 us (5.5 TB/s), 8: 17, 48: 65; 2 x 2048 -> 2048
+// 4.3 (3.9 TB/s; most of it the launch and the latency of the first loads).
 constexpr int WARPS = 8;
 
-template <int NT, bool GATED>
+template <int NT, int WAYS, bool GATED>
 __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
                                                              unsigned* err) {
   constexpr int ROWS = GATED ? 2 : 4, R = 4;
@@ -29,7 +30,9 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ptx::wait_for_previous();  // no memory of the caller is touched before this
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0u;  // this kernel never waits
-  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+  // all warps together: the same features for the whole block, which keeps their addresses uniform
+  const int way = WAYS == WARPS ? warp : warp % WAYS, group = WAYS == WARPS ? 0 : warp / WAYS;
+  const int64_t f0 = (static_cast<int64_t>(blockIdx.x) * (WARPS / WAYS) + group) * ROWS;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * NT;
   const float* X = static_cast<const float*>(g.A);
   const float* w[R];
@@ -43,7 +46,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
 #pragma unroll
   for (int t = 0; t < NT; ++t) x[t] = X + min(t0 + t, g.M - 1) * g.lda;
   float acc[R][NT] = {};
-  for (int64_t k = (warp * 32 + lane) * 4; k < g.K; k += WARPS * 128) {
+  for (int64_t k = (way * 32 + lane) * 4; k < g.K; k += WAYS * 128) {
     float4 wv[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) wv[r] = __ldcs(reinterpret_cast<const float4*>(w[r] + k));
@@ -77,16 +80,15 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
   }
   if (lane % (32 / V) == 0) sh[warp][lane / (32 / V)] = s[0];
   __syncthreads();
-  const int i = threadIdx.x;  // one result per thread
-  if (i >= ROWS * NT) return;
-  const int r = i % ROWS, t = i / ROWS;
+  if (way != 0 || lane >= ROWS * NT) return;  // one result per thread, of the first warp's lanes
+  const int r = lane % ROWS, t = lane / ROWS;
   const int64_t f = f0 + r, m = t0 + t;
   if (f >= g.Ncols || m >= g.M) return;
   float z = 0.f, u = 0.f;
 #pragma unroll
-  for (int k = 0; k < WARPS; ++k) {
-    z += sh[k][r * NT + t];
-    if (GATED) u += sh[k][(ROWS + r) * NT + t];
+  for (int k = 0; k < WAYS; ++k) {
+    z += sh[group * WAYS + k][r * NT + t];
+    if (GATED) u += sh[group * WAYS + k][(ROWS + r) * NT + t];
   }
   float v;
   dispatch_act(g.act, [&](auto tag) {
@@ -102,18 +104,42 @@ __global__ void __launch_bounds__(WARPS * 32) few_f32_kernel(const FfnGemm g,
   static_cast<float*>(g.C)[m * g.ldc + f] = v;
 }
 
-template <bool GATED>
+template <int NT, bool GATED>
 cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
   constexpr int ROWS = GATED ? 2 : 4;
-  const unsigned bx = static_cast<unsigned>((g.Ncols + ROWS - 1) / ROWS);
-  auto launch = [&](auto kernel, int nt) {
-    const dim3 grid(bx, static_cast<unsigned>((g.M + nt - 1) / nt));
+  const int64_t groups = (g.Ncols + ROWS - 1) / ROWS, token_tiles = (g.M + NT - 1) / NT;
+  auto blocks = [&](int ways) { return (groups * ways + WARPS - 1) / WARPS; };
+  auto launch = [&](auto kernel, int ways) {
+    const dim3 grid(static_cast<unsigned>(blocks(ways)), static_cast<unsigned>(token_tiles));
     return launch_kernel(kernel, grid, WARPS * 32, stream, g, err);
   };
-  if (g.M == 1) return launch(few_f32_kernel<1, GATED>, 1);
-  if (g.M == 2) return launch(few_f32_kernel<2, GATED>, 2);
-  if (g.M <= 4) return launch(few_f32_kernel<4, GATED>, 4);
-  return launch(few_f32_kernel<8, GATED>, 8);
+  // The cheapest by an estimate: waves of the blocks that fit on the SMs at once, each the steps of K
+  // and about two more for the sums.  (us with 8, 4, 2, 1 warps: 8 x 2048 -> 8192 21.6, 20.0, 19.1, 17.1;
+  // 12 x 1024 -> 2048 7.5, 5.8, 4.7, 7.1; 16 x 6000 -> 1500 19.9, 24.5, 25.5.)  One token always takes
+  // eight: the loads in flight decide (1 x 4096 -> 4096 13.2, 17.6 with two).
+  int ways = WARPS;
+  if (NT > 1) {
+    constexpr int PLACES = 152 * (NT == 2 ? 3 : 2);
+    int64_t best = INT64_MAX;
+    for (int w = WARPS; w >= 1; w /= 2) {
+      const int64_t cost = ((blocks(w) * token_tiles + PLACES - 1) / PLACES) *
+                           ((g.K + 128 * w - 1) / (128 * w) + 2);
+      if (cost < best) { best = cost; ways = w; }
+    }
+  }
+  if constexpr (NT > 1) {
+    if (ways == 1) return launch(few_f32_kernel<NT, 1, GATED>, 1);
+    if (ways == 2) return launch(few_f32_kernel<NT, 2, GATED>, 2);
+    if (ways == 4) return launch(few_f32_kernel<NT, 4, GATED>, 4);
+  }
+  return launch(few_f32_kernel<NT, WARPS, GATED>, WARPS);
+}
+template <bool GATED>
+cudaError_t few_f32(const FfnGemm& g, unsigned* err, cudaStream_t stream) {
+  if (g.M == 1) return few_f32<1, GATED>(g, err, stream);
+  if (g.M == 2) return few_f32<2, GATED>(g, err, stream);
+  if (g.M <= 4) return few_f32<4, GATED>(g, err, stream);
+  return few_f32<8, GATED>(g, err, stream);
 }
 
 // ---------------------------------------------------------------------------- column sums

@@ -141,6 +141,31 @@ def _close(got, want, tol, what):
 
 # tokens, widths: sums over many tokens beside short ones, many tiles (taken as tickets), operands whose
 # rows are copied, long sums of few and of many tokens, every kind at sizes of a real block
+# fp32 forward passes on both sides of the choice between dot products and tiles: one to eight warps per
+# sum, ragged token tiles and feature groups, K that ends inside a warp's step, the largest N
+F32_FORWARD = [(3, 132, 8196), (8, 2048, 2052), (13, 1028, 2004), (21, 516, 1028), (45, 4, 4), (48, 2052, 260),
+               (49, 260, 1004), (77, 6004, 132), (333, 1028, 1004), (301, 516, 1004), (4096, 36, 20),
+               (4097, 36, 20), (1000, 260, 516), (2, 1028, 4100)]
+
+
+@pytest.mark.parametrize("N,d,F", F32_FORWARD)
+def test_f32_forward(cuda_lib, N, d, F):
+    """Against plain products in float64 on the GPU, into a padded result whose padding stays."""
+    g = torch.Generator(device="cuda").manual_seed(N + d)
+    x, w, wu, b, r = (torch.randn(*s, generator=g, device="cuda") * k for s, k in (
+        ((N, d), 1.0), ((F, d), d ** -0.5), ((F, d), d ** -0.5), ((F,), 1.0), ((N, F), 1.0)))
+    z, u = x.double() @ w.double().t(), x.double() @ wu.double().t()
+    for act in ("gelu", "none"):
+        out = torch.full((N, F + 4), 7.0, device="cuda")
+        y, ws = api.lce_linear_forward(x, w, b, r, activation=act, out=out[:, :F])
+        api.lce_check_error(ws)
+        _close(y, _act64(z + b.double(), act) + r.double(), FWD["f32"], "y " + act)
+        assert torch.all(out[:, F:] == 7.0)
+    h, ws = api.lce_gated_forward(x, w, wu, activation="silu")
+    api.lce_check_error(ws)
+    _close(h, _act64(z, "silu") * u, FWD["f32"], "h")
+
+
 LARGE = [(16384, 128, 264, "bf16"), (8192, 132, 260, "f32"), (20000, 64, 5128, "bf16"), (4096, 1024, 4096, "bf16"),
          (2600, 1032, 2600, "bf16"), (2600, 520, 2616, "bf16"), (40, 16384, 520, "bf16"), (7, 12288, 1024, "f32"),
          (150, 8192, 2048, "bf16"), (150, 1024, 11008, "bf16"), (600, 9216, 520, "bf16"), (500, 4096, 516, "f32"),

@@ -9,9 +9,9 @@
 // chunks, last one first, so that what the first pass left in L2 is not read from memory again.  The
 // table of the arrays is a kernel argument: nothing is copied to the device, and a captured graph
 // holds its own table; lists longer than one table take several launches of each kind.
-// Both passes are bound by memory: the arrays are read twice and written once.  20 arrays of 137 MB take
-// 63.6 us (0.96 of the copy rate for the three passes), 1.25 GB 575 us (0.97), 0.6 MB 6.5 us (latency).
-// (Loading each vector of the next chunk as one is consumed was 2% slower from 100 MB on.)
+// Both passes are bound by memory: the arrays are read twice and written once.  20 arrays of 137 MB
+// take 62.5 us (0.97 of the copy rate for three passes), 1.25 GB 570-575 us (0.97), 0.6 MB 5.9 us
+// (latency).  (Loading each vector of the next chunk as one is consumed was 2% slower from 100 MB on.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -82,7 +82,8 @@ def test_workspace_sizes(lib):
     assert lib.lce_linear_workspace_size(50, 4104, 4096, 3, 0, 0) == H
     parts = lambda n, c: r256(n * r64(c) * 2 * 3)  # noqa: E731
     assert lib.lce_linear_workspace_size(8, 100, 200, 3, 0, 1) == H          # few tokens: no parts
-    assert lib.lce_linear_workspace_size(80, 100, 200, 0, 0, 1) == H + parts(80, 100) + parts(200, 100)
+    assert lib.lce_linear_workspace_size(80, 100, 200, 0, 0, 1) == H         # a small product: none either
+    assert lib.lce_linear_workspace_size(800, 1000, 2000, 0, 0, 1) == H + parts(800, 1000) + parts(2000, 1000)
     assert lib.lce_gated_workspace_size(80, 100, 200, 1, 1) == \
         H + parts(80, 100) + 2 * parts(200, 100) + 2 * parts(80, 200)
 

@@ -153,11 +153,12 @@ __device__ __forceinline__ void visit(const Chunk& c, const uint4 (&q)[UNROLL], 
 
 template <bool INF, int CAP>
 __global__ void __launch_bounds__(THREADS, 2)
-    norm_kernel(const __grid_constant__ Table<CAP> t, double* part) {
+    norm_kernel(const __grid_constant__ Table<CAP> t, double* part, unsigned* flags) {
   int64_t i = blockIdx.x;  // the grid is not larger than the number of chunks
   Chunk c = chunk_of(t, i);
   ptx::wait_for_previous();  // no memory of the caller is touched before this
   ptx::launch_dependents();  // its blocks take the places of this grid's as they end
+  if (blockIdx.x == 0 && threadIdx.x == 0) *flags = 0u;  // nothing here can fail on the device
   double sum = 0.0;
   unsigned m = 0;
   while (true) {
@@ -190,10 +191,14 @@ __device__ __forceinline__ float total_of(const double* part, int parts) {
 }
 
 template <bool INF>
-__global__ void __launch_bounds__(THREADS) total_kernel(const double* part, int parts, float* total) {
+__global__ void __launch_bounds__(THREADS) total_kernel(const double* part, int parts, float* total,
+                                                        unsigned* flags) {
   ptx::wait_for_previous();
   const float v = total_of<INF>(part, parts);
-  if (threadIdx.x == 0) *total = v;
+  if (threadIdx.x == 0) {
+    *total = v;
+    *flags = 0u;
+  }
 }
 
 template <typename E>
@@ -326,11 +331,13 @@ lce_status_t run(const void* const* grads, void* const* out, const int64_t* nume
                  const int32_t* dtypes, int64_t count, bool clip, float max_norm, float* total,
                  void* workspace, cudaStream_t stream) {
   double* part = reinterpret_cast<double*>(static_cast<char*>(workspace) + WS_HEADER_BYTES);
+  unsigned* flags = static_cast<unsigned*>(workspace);
   int parts = 0;
   cudaError_t e = for_tables<CAP>(grads, out, numels, dtypes, count, [&](const Table<CAP>& t) {
     const int blocks = static_cast<int>(std::min<int64_t>(t.first[t.count], MAX_BLOCKS));
     const cudaError_t r = traced(K_GRAD_NORM, stream, [&] {
-      return launch_kernel(norm_kernel<INF, CAP>, dim3(blocks), THREADS, stream, t, part + parts);
+      return launch_kernel(norm_kernel<INF, CAP>, dim3(blocks), THREADS, stream, t, part + parts,
+                           flags);
     });
     parts += blocks;
     return r;
@@ -338,7 +345,7 @@ lce_status_t run(const void* const* grads, void* const* out, const int64_t* nume
   if (e != cudaSuccess) return LCE_ERR_CUDA;
   if (!clip || parts == 0) {
     e = traced(K_GRAD_NORM, stream, [&] {
-      return launch_kernel(total_kernel<INF>, dim3(1), THREADS, stream, part, parts, total);
+      return launch_kernel(total_kernel<INF>, dim3(1), THREADS, stream, part, parts, total, flags);
     });
     return e == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
   }

@@ -332,7 +332,8 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
  * lce_clip_grad_norm then writes out[i] = grads[i] * c, c = min(1, max_norm / (total + 1e-6)) in
  * fp32, rounded once; out[i] may be grads[i] (out == NULL: all in place), any other overlap of an
  * output with an input or output is not allowed.  In place with c = 1 nothing is written.  A NaN
- * total makes every output NaN, an infinite one makes c = 0.
+ * total makes every output NaN, an infinite one makes c = 0, whatever max_norm is (infinite: no limit,
+ * finite gradients stay as they are).
  * The order of every sum is fixed by the counts and the device: results are reproducible.
  */
 typedef enum { LCE_NORM_L2 = 0, LCE_NORM_INF = 1 } lce_norm_t;

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   ptx::launch_dependents();
   const float v = total_of<INF>(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *total = v;
-  const float r = max_norm / (v + 1e-6f);
+  const float r = isinf(v) ? 0.f : max_norm / (v + 1e-6f);  // also where max_norm is infinite
   const float f = r > 1.f ? 1.f : r;  // NaN stays
   while (true) {
     if (f != 1.f || c.in != c.out) {

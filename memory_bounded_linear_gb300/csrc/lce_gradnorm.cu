@@ -9,9 +9,10 @@
 // chunks, last one first, so that what the first pass left in L2 is not read from memory again.  The
 // table of the arrays is a kernel argument: nothing is copied to the device, and a captured graph
 // holds its own table; lists longer than one table take several launches of each kind.
-// Both passes are bound by memory: the arrays are read twice and written once.  20 arrays of 137 MB
-// take 62.5 us (0.97 of the copy rate for three passes), 1.25 GB 570-575 us (0.97), 0.6 MB 5.9 us
-// (latency).  (Loading each vector of the next chunk as one is consumed was 2% slower from 100 MB on.)
+// Both passes are bound by memory: the arrays are read twice and written once.  Inside a captured graph
+// 20 arrays of 137 MB take 63.1 us (0.97 of the copy rate for three passes), 1.25 GB 578 us (0.96), 0.6
+// MB 6.2 us (latency).  (Loading each vector of the next chunk as one is consumed was 2% slower from 100
+// MB on.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -244,14 +245,14 @@ template <bool INF, int CAP>
 __global__ void __launch_bounds__(THREADS, 2)
     scale_kernel(const __grid_constant__ Table<CAP> t, const double* part, int parts, float max_norm,
                  float* total) {
-  // The first chunk is read while the partials are summed, and before the launch that writes them has
-  // ended: it reads the same arrays, and was past its own wait when it let this one begin.
   int64_t i = t.first[t.count] - 1 - blockIdx.x;  // the grid is not larger than the number of chunks
   Chunk c = chunk_of(t, i);
-  uint4 q[UNROLL];
-  load<true>(c, q);
+  // No memory of the caller is touched before this, the gradients neither: the kernel that wrote them
+  // lies two launches back, and only a wait of its own makes those writes visible to this kernel.
   ptx::wait_for_previous();
   ptx::launch_dependents();
+  uint4 q[UNROLL];
+  load<true>(c, q);  // in flight while the partials are summed
   const float v = total_of<INF>(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *total = v;
   const float r = isinf(v) ? 0.f : max_norm / (v + 1e-6f);  // also where max_norm is infinite
@@ -278,7 +279,7 @@ cudaError_t for_tables(const void* const* grads, void* const* out, const int64_t
   Table<CAP> t;
   t.vectors = THREADS;
   // a chunk for every SM at most, while that is enough: a block of the second pass then fits beside one
-  // of the first and begins with it (27 arrays of 2 MB 6.0 us, 8.3 with twice as many smaller chunks)
+  // of the first and begins with it (27 arrays of 2 MB 6.2 us, 8.7 with twice as many smaller chunks)
   while (t.vectors < THREADS * UNROLL && bytes / (16.0 * t.vectors) + count > MAX_BLOCKS / 2)
     t.vectors *= 2;
   t.count = 0;

@@ -443,8 +443,9 @@ def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: 
                        workspace: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None):
     """Scales a non-empty list of gradients by min(1, max_norm / (total + 1e-6)), total their global
-    norm: in place, or into ``out`` (tensors of the same dtypes, shapes and strides).  Nothing is
-    read back to the host.  Returns (total [] fp32 on the device, the scaled tensors, workspace)."""
+    norm: in place, or into ``out`` (tensors of the same dtypes, shapes and strides; no tensor that is
+    written may share memory with another one of the call).  Nothing is read back to the host.
+    Returns (total [] fp32 on the device, the scaled tensors, workspace)."""
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
     if not isinstance(grads, (list, tuple)):
@@ -457,10 +458,11 @@ def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: 
 def clip_grad_norm_(parameters, max_norm: float, norm: str = "l2") -> torch.Tensor:
     """Clips the gradients of ``parameters`` (a tensor or an iterable of tensors; those without a
     gradient are passed over) in place to a global norm of at most max_norm; returns the norm
-    before clipping, on the device (a CPU zero when there is no gradient)."""
+    before clipping, on the device (a CPU zero when there is no gradient).  A gradient that appears
+    twice, as of a parameter in two lists, counts and is scaled once."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    grads = [p.grad for p in parameters if p.grad is not None]
+    grads = list({id(g): g for g in (p.grad for p in parameters) if g is not None}.values())
     if not grads:
         return torch.zeros(())
     return lce_clip_grad_norm(grads, max_norm, norm=norm)[0]

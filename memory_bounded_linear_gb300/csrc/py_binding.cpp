@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -233,6 +234,36 @@ PyObject* gated_backward(PyObject* const* a) {
   return st == LCE_OK ? tuple_of(dx, dwg, dwu, ws) : status(st);
 }
 
+// Refuses outputs that share memory with another output, or with an input that is not the same array:
+// blocks that run at the same time would read values that others have scaled already.  Inputs may
+// share memory with one another where nothing is written to it.
+void check_overlap(const std::vector<const void*>& in, const std::vector<void*>& out,
+                   const std::vector<int64_t>& bytes) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * in.size());
+  auto add = [&](const void* p, int64_t n, bool written) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    if (n > 0) spans.push_back(Span{b, b + static_cast<uintptr_t>(n), written});
+  };
+  for (size_t i = 0; i < in.size(); ++i) {
+    const void* o = out.empty() ? in[i] : out[i];
+    add(o, bytes[i], true);
+    if (o != in[i]) add(in[i], bytes[i], false);
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t read = 0, written = 0;  // ends of what came so far
+  for (const Span& s : spans) {
+    if (s.begin < written || (s.written && s.begin < read))
+      refuse(PyExc_ValueError, "an array that is written overlaps another one of the call");
+    uintptr_t& end = s.written ? written : read;
+    end = std::max(end, s.end);
+  }
+}
+
 // (gradients, out or None, norm, max_norm or None, workspace) -> (total, workspace) or a status;
 // without max_norm the norm alone.
 PyObject* clip(PyObject* const* a) {
@@ -252,7 +283,7 @@ PyObject* clip(PyObject* const* a) {
   if (!first.is_cuda()) refuse(PyExc_ValueError, "gradients must be CUDA tensors");
   std::vector<const void*> in(n);
   std::vector<void*> out;
-  std::vector<int64_t> numel(n);
+  std::vector<int64_t> numel(n), bytes(n);
   std::vector<int32_t> dt(n);
   for (Py_ssize_t i = 0; i < n; ++i) {
     const at::Tensor& t = tensor(grads.at(i), "a gradient");
@@ -263,6 +294,7 @@ PyObject* clip(PyObject* const* a) {
       refuse(PyExc_ValueError, "gradients must be dense (strides ", t.strides(), " of ", t.sizes(), ")");
     in[i] = t.data_ptr();
     numel[i] = t.numel();
+    bytes[i] = t.nbytes();
   }
   if (a[1] != Py_None) {
     const Held outs(a[1]);
@@ -276,6 +308,7 @@ PyObject* clip(PyObject* const* a) {
       out[i] = o.data_ptr();
     }
   }
+  if (a[3] != Py_None) check_overlap(in, out, bytes);
   const lce_norm_t norm = static_cast<lce_norm_t>(PyLong_AsLong(a[2]));
   const size_t need = lce_grad_norm_workspace_size(n);
   if (need == 0) return status(LCE_ERR_UNSUPPORTED_SHAPE);

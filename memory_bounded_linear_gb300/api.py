@@ -450,6 +450,8 @@ def lce_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, norm: 
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)
+    if out is not None and not isinstance(out, (list, tuple)):
+        out = list(out)
     total, ws = _call("lce_clip_grad_norm", _lib.native().clip, stream, grads, out, _norm(norm),
                       float(max_norm), workspace)
     return total, list(grads if out is None else out), ws

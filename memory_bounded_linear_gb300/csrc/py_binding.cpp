@@ -113,6 +113,12 @@ PyObject* wrap(const at::Tensor& t) {
 }
 PyObject* status(lce_status_t st) { return PyLong_FromLong(st); }
 
+// Tells autograd that a caller's tensor is written: a backward pass that saved its old values then
+// raises instead of using the new ones.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 template <typename... T>
 PyObject* tuple_of(const T&... t) {
   PyObject* items[] = {wrap(t)...};
@@ -154,7 +160,8 @@ PyObject* linear_forward(PyObject* const* a) {
   if (need == 0) return status(LCE_ERR_UNSUPPORTED_SHAPE);
   const c10::cuda::CUDAGuard guard(x.device());
   const at::Tensor ws = workspace(a[6], need, x);
-  if (!out.defined()) out = at::empty({s.N, s.width}, x.options());
+  if (out.defined()) written(out);
+  else out = at::empty({s.N, s.width}, x.options());
   const lce_status_t st =
       lce_linear_forward(ptr(x), ldx, ptr(w), ptr(bias), ptr(res), ldr, s.N, s.d, s.width, act, s.dt,
                          ptr(out), ldy, ptr(ws), ws.numel(), stream_of(x));
@@ -200,7 +207,8 @@ PyObject* gated_forward(PyObject* const* a) {
   if (need == 0) return status(LCE_ERR_UNSUPPORTED_SHAPE);
   const c10::cuda::CUDAGuard guard(x.device());
   const at::Tensor ws = workspace(a[5], need, x);
-  if (!out.defined()) out = at::empty({s.N, s.width}, x.options());
+  if (out.defined()) written(out);
+  else out = at::empty({s.N, s.width}, x.options());
   const lce_status_t st =
       lce_gated_forward(ptr(x), ldx, ptr(wg), ptr(wu), s.N, s.d, s.width, act, s.dt, ptr(out), ldh,
                         ptr(ws), ws.numel(), stream_of(x));
@@ -316,6 +324,10 @@ PyObject* clip(PyObject* const* a) {
   const at::Tensor ws = workspace(a[4], need, first);
   const at::Tensor total = at::empty({}, first.options().dtype(at::kFloat));
   float* tp = static_cast<float*>(total.data_ptr());
+  if (a[3] != Py_None) {
+    const Held written_to(a[1] == Py_None ? a[0] : a[1]);
+    for (Py_ssize_t i = 0; i < n; ++i) written(tensor(written_to.at(i), "an output"));
+  }
   const lce_status_t st =
       a[3] == Py_None
           ? lce_grad_norm(in.data(), numel.data(), dt.data(), n, norm, tp, ptr(ws), ws.numel(),

@@ -1,5 +1,6 @@
 """Build ``liblce.so`` (the C-ABI library) for sm_103a with nvcc, and ``_native.so`` (its binding to
 torch tensors for the operators called once per layer and token) with the host compiler, in-tree.
+liblce.so needs nothing but nvcc: it is linked first, and without torch the binding is left out.
 
 Each translation unit is compiled in parallel to an object file under ``_build/`` at the
 repository root, then linked (CUDA runtime linked statically) into
@@ -9,6 +10,7 @@ repository root, then linked (CUDA runtime linked statically) into
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -49,8 +51,11 @@ def _compile(src: str, ptxas_verbose: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
-def _compile_binding() -> str:
-    """Object file of the binding; torch's headers and its C++ ABI come from the installed torch."""
+def _compile_binding() -> str | None:
+    """Object file of the binding, None without torch; torch's headers and its C++ ABI come from the
+    installed torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     import torch
     from torch.utils import cpp_extension
 
@@ -85,7 +90,6 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), SOURCES))
-        binding_obj = binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for (_, log), src in zip(results, SOURCES):
@@ -98,7 +102,11 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    obj = binding.result()
+    if obj is None:
+        print("torch is not installed: _native.so, the binding to its tensors, is not built", file=sys.stderr)
+    else:
+        _link_binding(obj)
     return LIB
 
 

@@ -26,6 +26,7 @@
 #include "lce_act.cuh"
 #include "lce_ffn.h"
 #include "lce_internal.h"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -278,18 +279,18 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int
 
 template <bool GATED>
 cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t stream) {
-  static bool attr_set[kMaxDevices];
-  int dev = 0;
+  static PerDevice<kMaxDevices> attr_set;
+  int dev = 0, set = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<GATED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
-    if (e != cudaSuccess) {
-      set_error_detail("shared-memory attribute of the few-token kernel: %s", cudaGetErrorName(e));
-      return e;
-    }
-    attr_set[dev] = true;
-  }
+  cudaError_t e = attr_set.get(dev, [](int* done) {
+    *done = 1;
+    const cudaError_t r = cudaFuncSetAttribute(ffn_few_kernel<GATED>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ONE);
+    if (r != cudaSuccess)
+      set_error_detail("shared-memory attribute of the few-token kernel: %s", cudaGetErrorName(r));
+    return r;
+  }, &set);
+  if (e != cudaSuccess) return e;
   constexpr int W = GATED ? 2 : 1;
   Params p{};
   p.N = static_cast<int>(g.M);
@@ -347,7 +348,7 @@ cudaError_t launch(const FfnGemm& g, unsigned* err, int num_sms, cudaStream_t st
   attr[1] = dependent_launch();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATED>, maps, p);
+  e = cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATED>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     set_error_detail("launch of the few-token kernel (%lld tiles, split %d): %s",

@@ -56,6 +56,7 @@
 #include "lce_act.cuh"
 #include "lce_ffn.h"
 #include "lce_internal.h"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -893,34 +894,45 @@ bool operand(CUtensorMap* m, const FfnOperand& o, bool mn, int rows, const char*
                   ps, what);
 }
 
-// Largest number of clusters of `pairs` CTA pairs that the device holds at once (every mode's kernel
-// takes the same room).
+// The device that is current, one that this library keeps state for.
+cudaError_t current_device(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return *dev >= 0 && *dev < kMaxDevices ? cudaSuccess : cudaErrorInvalidDevice;
+}
+
+// Largest number of clusters of 1 .. MAX_SPLIT CTA pairs that the device holds at once (every mode's
+// kernel takes the same room), for the powers of two.
+struct ClusterLimits {
+  int of[MAX_SPLIT + 1] = {};
+};
 template <bool F32>
-int max_clusters(int pairs) {
-  static int cached[MAX_SPLIT + 1];
-  if (cached[pairs] == 0) {
-    const auto kernel = ffn_tc_kernel<FFN_GRADS, F32, true>;
-    constexpr int bytes = SMEM_BYTES;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs, 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = bytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * pairs;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-      (void)cudaGetLastError();
-      n = 0;
-    }
-    cached[pairs] = n > 0 ? n : -1;
+cudaError_t cluster_limits(int dev, ClusterLimits* limits) {
+  static PerDevice<kMaxDevices> cached[MAX_SPLIT + 1];
+  for (int pairs = 2; pairs <= MAX_SPLIT; pairs *= 2) {
+    auto query = [&](int* n) {
+      const auto kernel = ffn_tc_kernel<FFN_GRADS, F32, true>;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * pairs, 1, 1);
+      cfg.blockDim = dim3(THREADS, 1, 1);
+      cfg.dynamicSmemBytes = SMEM_BYTES;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2 * pairs;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+      if (e != cudaSuccess)
+        set_error_detail("clusters of %d CTAs of a feed-forward kernel: %s", 2 * pairs, cudaGetErrorName(e));
+      return e;
+    };
+    const cudaError_t e = cached[pairs].get(dev, query, &limits->of[pairs]);
+    if (e != cudaSuccess) return e;
   }
-  return std::max(cached[pairs], 0);
+  return cudaSuccess;
 }
 
 // How a launch's tiles and sums are cut.  It is chosen from all products of the launch, asked for or
@@ -939,7 +951,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // partial sums at 14 bytes per cycle and SM (the rate distributed shared memory showed: 5 us for a
 // tile cut in four) after about 1,500 of synchronisation.
 template <bool F32>
-Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
+Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units, const ClusterLimits& limits) {
   Plan best;
   for (int bn = TILE; bn >= TILE / 2; bn /= 2) {
     const double step_cost = (bn == TILE ? 528.0 : 390.0) * (F32 ? 6 * F32_STEP : 1);
@@ -978,7 +990,7 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
           slowest = std::max(slowest, whole[j] ? ceil_div(steps[j], k) * step_cost + join + finish / k
                                                : steps[j] * step_cost + finish);
         }
-        if (!any || clusters > max_clusters<F32>(k) || slowest >= best.cost) continue;
+        if (!any || clusters > limits.of[k] || slowest >= best.cost) continue;
         best.cost = slowest;
         best.bn = bn;
         best.split = k;
@@ -991,21 +1003,22 @@ Plan choose_plan(const FfnTc* jobs, int njobs, bool gated, int units) {
 
 template <int MODE, bool F32>
 cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stream) {
-  static bool attr_set[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
+  static PerDevice<kMaxDevices> attr_set;
+  int dev = 0, set = 0;
+  cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  e = attr_set.get(dev, [](int* done) {
+    *done = 1;
+    cudaError_t r = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, true>,
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(ffn_tc_kernel<MODE, F32, true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) {
-      set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(e));
-      return e;
-    }
-    attr_set[dev] = true;
-  }
+    if (r != cudaSuccess)
+      set_error_detail("shared-memory attribute of a feed-forward kernel: %s", cudaGetErrorName(r));
+    return r;
+  }, &set);
+  if (e != cudaSuccess) return e;
   int clusters = 0;
   for (int j = 0; j < p.njobs; ++j)
     clusters += static_cast<int>(p.job[j].whole ? p.job[j].num_tiles : ceil_div(p.job[j].num_tiles, p.split));
@@ -1024,8 +1037,8 @@ cudaError_t launch(const FMaps& maps, KParams& p, int num_sms, cudaStream_t stre
   attr[1] = dependent_launch();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, true>, maps, p)
-                              : cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, false>, maps, p);
+  e = p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, true>, maps, p)
+                  : cudaLaunchKernelEx(&cfg, ffn_tc_kernel<MODE, F32, false>, maps, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     set_error_detail("launch of a feed-forward product (mode %d, %d tiles, split %d): %s", MODE,
@@ -1140,7 +1153,12 @@ cudaError_t run_planned(const FfnTc* jobs, int njobs, unsigned* header, CallStat
   const bool gated = jobs[0].mode == FFN_GATED || jobs[0].mode == FFN_GATED_DGU;
   for (int i = 0; i < njobs; ++i)
     if (ceil_div(jobs[i].K, BK) > (1 << 25)) return cudaErrorInvalidValue;  // widths end at 2^31
-  const Plan all = choose_plan<F32>(jobs, njobs, gated, num_sms / 2);
+  int dev = 0;
+  ClusterLimits limits;
+  cudaError_t e = current_device(&dev);
+  if (e == cudaSuccess) e = cluster_limits<F32>(dev, &limits);
+  if (e != cudaSuccess) return e;
+  const Plan all = choose_plan<F32>(jobs, njobs, gated, num_sms / 2, limits);
   if (njobs > 1) {
     FfnTc group[2][MAX_JOBS];
     int n[2] = {0, 0};
@@ -1149,15 +1167,15 @@ cudaError_t run_planned(const FfnTc* jobs, int njobs, unsigned* header, CallStat
       group[k][n[k]++] = jobs[i];
     }
     if (n[0] && n[1]) {
-      const Plan plan[2] = {choose_plan<F32>(group[0], n[0], gated, num_sms / 2),
-                            choose_plan<F32>(group[1], n[1], gated, num_sms / 2)};
+      const Plan plan[2] = {choose_plan<F32>(group[0], n[0], gated, num_sms / 2, limits),
+                            choose_plan<F32>(group[1], n[1], gated, num_sms / 2, limits)};
       if (plan[0].cost + plan[1].cost + kLaunch < all.cost) {
         int launches = 0;
         for (int k = 0; k < 2; ++k) {
           bool asked = false;
           for (int i = 0; i < n[k]; ++i) asked |= group[k][i].C != nullptr;
           if (!asked) continue;
-          const cudaError_t e = run<F32>(group[k], n[k], plan[k], header, state, num_sms, stream);
+          e = run<F32>(group[k], n[k], plan[k], header, state, num_sms, stream);
           if (e != cudaSuccess) return e;
           ++launches;
         }

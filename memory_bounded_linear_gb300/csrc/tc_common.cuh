@@ -22,7 +22,6 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;  // a wait longer than 2 s is 
 // Tiles handed out by the dynamic scheduler wait in a small ring until every role has read them.
 constexpr int TQ = 4;
 
-
 // Suspend-time hint of every barrier wait (ns): a waiting thread sleeps in the try_wait until the
 // phase completes, up to this long, instead of returning early and polling again.  Measured 1.0-
 // 1.5% faster steps than the instruction's default, with or without the power cap.
@@ -102,8 +101,7 @@ struct TileQueue {
 
   // Scheduler: posts `ticket` (taken from the counter sched[0] beforehand) to both CTAs, or -1
   // when it is past the last tile.  Returns what was posted (-1 also after a timeout); the last
-  // unit to receive -1 clears the counters for the next launch.  sched may be null: the caller
-  // draws its tickets without counters.
+  // unit to receive -1 clears the counters for the next launch.
   __device__ __forceinline__ int post(unsigned ticket, unsigned* sched, int num_tiles, int units) {
     const uint32_t empty = ptx::smem_addr(&ctl->tq_empty[slot]);
     if (!wait_bar<PAIR>(empty, ph ^ 1u, abort_flag, err)) return -1;
@@ -116,7 +114,7 @@ struct TileQueue {
     }
     ptx::mbar_arrive(full);
     advance();
-    if (t < 0 && sched && atomicAdd(&sched[1], 1u) == static_cast<unsigned>(units - 1)) {
+    if (t < 0 && atomicAdd(&sched[1], 1u) == static_cast<unsigned>(units - 1)) {
       atomicExch(&sched[0], 0u);
       atomicExch(&sched[1], 0u);
     }

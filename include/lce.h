@@ -254,6 +254,8 @@ lce_status_t lce_forward_static_scratch(const void* H, const void* W, const int6
  *   - Outputs are bitwise reproducible for a fixed device and fixed shapes.  A row of Y or H does
  *     not depend on the other rows' values, but its summation order may differ between the call
  *     for a few tokens and the call for many.
+ *   - With LCE_F32 a value of magnitude below 2^-109 enters the tensor-core products with fewer
+ *     than 24 bits (its last part falls below bf16's range).
  *   - An inf or NaN in an operand makes the outputs it takes part in inf or NaN.  With LCE_F32 an
  *     inf may come out as NaN: operands are summed in parts.  Where a ReLU is 0 the gradient before it
  *     is 0 whatever the outgoing one holds.
@@ -286,7 +288,7 @@ lce_status_t lce_linear_forward(const void* X, int64_t ldx, const void* W, const
  * (the residual's gradient is dY).  The pre-activations are recomputed, not kept from the forward
  * pass; with LCE_ACT_NONE there is nothing to recompute and bias is not read.  dX [N x d_in], dW
  * [d_out x d_in] and dbias [d_out] are dense; a gradient whose pointer is NULL is not computed.
- * For LCE_BF16 dZ is rounded to bf16 as an operand of the products.
+ * For LCE_BF16 dZ is rounded to bf16, and the rounded values enter the products and the column sums.
  */
 lce_status_t lce_linear_backward(const void* X, int64_t ldx, const void* W, const void* bias,
                                  const void* dY, int64_t ldy, int64_t N, int64_t d_in,
@@ -324,9 +326,10 @@ lce_status_t lce_gated_backward(const void* X, int64_t ldx, const void* Wg, cons
  * HOST arrays of `count` entries that are read during the call: device pointers, element counts
  * (0 allowed, the pointer may then be NULL) and types (LCE_BF16 or LCE_F32, mixed freely).  The
  * device arrays are dense and aligned to their element size; 16-byte alignment is not needed.
- *   LCE_NORM_L2   total = sqrt(sum of g^2): squares in fp32, summed per thread over at most 64
- *                 values in fp32 and beyond that in fp64; squares that pass fp32 (|g| > 1.8e19)
- *                 count as inf
+ *   LCE_NORM_L2   total = sqrt(sum of g^2): squares in fp32, summed per thread over at most 66
+ *                 values in fp32 and beyond that in fp64.  Such a sum that passes fp32 counts as
+ *                 inf (never with all |g| below 2e18); squares lose bits where |g| is below 1e-19
+ *                 and are 0 below 2.6e-23
  *   LCE_NORM_INF  total = max |g|
  * A NaN anywhere gives a NaN total.  total_norm is a device fp32 scalar.
  * lce_clip_grad_norm then writes out[i] = grads[i] * c, c = min(1, max_norm / (total + 1e-6)) in

@@ -293,7 +293,8 @@ def lce_linear_forward(X, W, bias=None, residual=None, *, activation: str = "non
                        workspace: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None):
     """Y = act(X W^T + bias) + residual.  X [N, d_in], residual and out [N, d_out] may have a row
-    stride; W [d_out, d_in] and bias [d_out] are contiguous.  out may be residual itself.
+    stride; W [d_out, d_in] and bias [d_out] are contiguous.  out may be residual itself and shares
+    no element with any other argument.
     Returns (Y, workspace)."""
     return _call("lce_linear_forward", _lib.native().linear_forward, stream, X, W, bias, residual,
                  _activation(activation), out, workspace)
@@ -313,7 +314,7 @@ def lce_gated_forward(X, Wg, Wu, *, activation: str = "silu", out: Optional[torc
                       workspace: Optional[torch.Tensor] = None,
                       stream: Optional[torch.cuda.Stream] = None):
     """H = act(X Wg^T) * (X Wu^T).  X [N, d] and out [N, F] may have a row stride; Wg and Wu [F, d]
-    are contiguous.  Returns (H, workspace)."""
+    are contiguous; out shares no element with another argument.  Returns (H, workspace)."""
     return _call("lce_gated_forward", _lib.native().gated_forward, stream, X, Wg, Wu,
                  _activation(activation), out, workspace)
 

@@ -4,7 +4,8 @@ liblce.so needs nothing but nvcc: it is linked first, and without torch the bind
 
 Each translation unit is compiled in parallel to an object file under ``_build/`` at the
 repository root, then linked (CUDA runtime linked statically) into
-``memory_bounded_linear_gb300/liblce.so``.  Usage: ``python -m memory_bounded_linear_gb300.csrc.build``.
+``memory_bounded_linear_gb300/liblce.so``.  Usage: ``python -m memory_bounded_linear_gb300.csrc.build``,
+or without torch, which the package imports, ``python memory_bounded_linear_gb300/csrc/build.py``.
 """
 
 from __future__ import annotations

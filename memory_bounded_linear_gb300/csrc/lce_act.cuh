@@ -50,8 +50,9 @@ __device__ __forceinline__ V fast_sigmoid(V x, float c = 1.f) {
 }
 
 // Phi(x) and e = exp(-x^2 / 2), for bf16 results.  The upper tail Q(y) = erfc(y / sqrt 2) / 2 is
-// e t P(t) / 2 with t = 1 / (1 + 0.46 y / sqrt 2); the degree-5 P was fitted to exp(z^2) erfc(z) / t on
-// z >= 0 (least squares in t, reweighted towards the largest relative error, 1.8e-5).  One exponential
+// e t P(t) / 2 with t = 1 / (1 + 0.46 y / sqrt 2), Hastings' form; the degree-5 P was fitted to exp(z^2)
+// erfc(z) / t on z >= 0 (least squares in t, reweighted towards the largest relative error as in
+// Lawson's algorithm; 1.8e-5).  One exponential
 // and one quotient serve Phi and the density in its derivative.
 template <typename V>
 __device__ __forceinline__ V normal_cdf(V x, V& e) {

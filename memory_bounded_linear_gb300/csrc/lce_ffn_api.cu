@@ -35,13 +35,17 @@ bool sizes_ok(int64_t N, int64_t d, int64_t width, lce_dtype_t dt) {
 }
 
 // Whether a forward product of N tokens runs as a weight stream (lce_ffn_few.cu; fp32:
-// lce_ffn_simt.cu) rather than in tiles of 256 tokens (lce_ffn_tc.cu).  us, stream / tiles:
+// lce_ffn_simt.cu) rather than in tiles of 256 tokens (lce_ffn_tc.cu).  us inside a captured graph,
+// stream / tiles:
 //   linear 128 x 8192 -> 4096 18 / 24, 128 x 5224 -> 13384 45 / 39, 160 x 11008 -> 4096 24 / 30, 192: 28 / 31;
 //     160 x 4096 -> 11008 26 / 25: the stream cuts long K loops into more pieces
 //   gated 128 x 4096 x 11008 40 / 47, 160: 42 / 47, 192: 49 / 48 (a tile for each of more than half the
 //     SMs, no joining); 48 x 4096 x 8192 27 / 27, 96: 32 / 27 (two sums to join per tile);
 //     96 x 2048 x 1024 8.7 / 11.9, 128: 22 / 12 (its partial sums no longer fit)
-//   fp32 linear 32 x 2048 -> 8192 49 / 67, 64: 83 / 67, 40 x 4096 -> 4096 69 / 80; small products, for
+//   fp32 linear 32 x 2048 -> 8192 50 / 65, 48: 64 / 65, 64: 83 / 65, 40 x 4096 -> 4096 69 / 80: up to 48
+//     tokens, the crossing of weights that fit in L2.  The stream reads them once per eight tokens, so
+//     that larger ones cross at about 34: 6144 -> 16384 with 32 tokens 293 / 322, 40: 390 / 322, 48:
+//     471 / 322; 4096 -> 16384 32: 207 / 220, 48: 315 / 220; gated 32 x 6144 -> 16384 583 / 633.  Small products, for
 //     which the tiles take about 12 us + 6 per 1000 of d: 64 x 512 -> 1024 4.5 / 14, 256: 14.9 / 14.5,
 //     100 x 1024 -> 1024 12.6 / 16.5, 500 x 256 -> 512 10.0 / 12.2, 1000: 17.4 / 12.4, 100 x 6000 -> 512
 //     31 / 48; a result costs about as much as 100 more of d (4096 x 128 -> 144 15.9 / 10.0)

@@ -14,12 +14,14 @@ namespace lce {
 namespace {
 
 // ---------------------------------------------------------------- fp32 products of a few tokens
-// Bound by reading the weights once (HBM), from about eight tokens on by the products.  A warp computes
-// ROWS features (4; gated 2 of Wg and 2 of Wu) for NT tokens, or WAYS warps of a block together: they
-// take 512-byte pieces of K in turn, lanes four elements each, and each weight vector loaded serves NT
-// tokens from registers (X comes from L1/L2).  The lanes' sums meet by shuffles, the warps' in shared
-// memory, in a fixed order.  1 x 2048 -> 8192 takes 12.3 us (5.5 TB/s), 8: 17, 48: 65; 2 x 2048 -> 2048
-// 4.3 (3.9 TB/s; most of it the launch and the latency of the first loads).
+// Up to eight tokens bound by reading the weights once (HBM).  A warp computes ROWS features (4; gated 2
+// of Wg and 2 of Wu) for NT tokens, at most eight, or WAYS warps of a block together: they take 512-byte
+// pieces of K in turn, lanes four elements each, and each weight vector loaded serves NT tokens from
+// registers (X comes from L1/L2).  The lanes' sums meet by shuffles, the warps' in shared memory, in a
+// fixed order.  Every further tile of eight tokens reads all weights again, from L2 at best: the token
+// tile is the slower grid index.  Inside a captured graph 1 x 2048 -> 8192 takes 12.3 us (5.5 TB/s), 8: 17,
+// 16: 29, 32: 50, 48: 64; 6144 -> 16384 (403 MB) 8: 85, 16: 162, 32: 293, 48: 471; 2 x 2048 -> 2048 4.4
+// (3.8 TB/s; most of it the launch and the latency of the first loads).
 constexpr int WARPS = 8;
 
 template <int NT, int WAYS, bool GATED>

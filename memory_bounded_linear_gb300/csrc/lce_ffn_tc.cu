@@ -40,9 +40,10 @@
 // while the other leaves); with long K they have one box and six stages.
 //
 // Bound: tensor pipe for many tokens (products hide the epilogue from K = 1024 on; at K = 512 a tile's
-// epilogue takes 11,000 cycles, its products 4,100).  Measured: gated backward 16384 x 4096 -> 16384
-// 7.1 ms (1,860 TFLOP/s), linear 4096 x 8192 -> 2048 84 us (1,630: 128 tiles on 76 pairs), gated forward
-// 777 x 4096 -> 10952 97 us (1,430: four row tiles for 3.04).
+// epilogue takes 11,000 cycles, its products 4,100).  Measured inside a captured graph, and as single
+// calls: gated backward 16384 x 4096 -> 16384 7.0-7.1 ms (1,850-1,880 TFLOP/s) and 7.7-7.8, linear 4096 x
+// 8192 -> 2048 83 us (1,650: 128 tiles on 76 pairs) and 93, gated forward 777 x 4096 -> 10952 96 us (1,450:
+// four row tiles for 3.04) and 111.
 // Ragged edges: TMA zero-fills loads and clips stores.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -60,7 +60,7 @@ __device__ __forceinline__ int find(const Table<CAP>& t, int64_t chunk) {
 __device__ __forceinline__ unsigned mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 struct Acc {
-  float s;     // sum of squares of at most 64 values (and up to 14 at the unaligned ends)
+  float s;     // sum of squares of at most 64 values (and two at the unaligned ends)
   unsigned m;  // largest magnitude
   template <bool INF>
   __device__ __forceinline__ void add(float x) {

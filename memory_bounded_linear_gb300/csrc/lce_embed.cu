@@ -180,11 +180,14 @@ __global__ void __launch_bounds__(SORT_THREADS) embedding_count_kernel(const Sor
     a.counts_clear[static_cast<int64_t>(blockIdx.x) * MAX_BINS + i] = 0u;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.tile;
   const int64_t i1 = min(i0 + a.tile, a.N);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_THREADS) {
-    const unsigned d = key_of(a.tokens[i], a) & (n_bins - 1);
+  // a warp goes on as one, whichever of its lanes are within the tile: all of them take part in the matching
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = i0 + (threadIdx.x - lane); i < i1; i += SORT_THREADS) {
+    const bool in = i + lane < i1;
+    const unsigned d = in ? key_of(a.tokens[i + lane], a) & (n_bins - 1) : 0xffffffffu;
     // frequent tokens come many at a time: one addition for each digit of a warp
-    const unsigned same = __match_any_sync(__activemask(), d);
-    if ((threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&bins[d], __popc(same));
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    if (in && lane == __ffs(same) - 1) atomicAdd(&bins[d], __popc(same));
   }
   __syncthreads();
   unsigned* out = const_cast<unsigned*>(a.counts) + static_cast<int64_t>(blockIdx.x) * MAX_BINS;

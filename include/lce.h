@@ -376,8 +376,10 @@ size_t lce_layer_norm_workspace_size(int64_t N, int64_t d, lce_dtype_t dtype);
 /*
  * Y [N x d] = (X - mean) / sqrt(var + eps) * weight + bias, mean and var (divided by d) over each row of
  * X [N x d].  weight [d] and bias [d] may be NULL (1 and 0).  eps is finite and above 0 (without it a row
- * of equal values would be 0 / 0, and rounding decide).  An inf or NaN in a row makes that row NaN;
- * differences to the mean beyond 1e16 may overflow in the variance.  Nothing but X is needed for the backward pass.
+ * of equal values would be 0 / 0, and rounding decide).  An inf or NaN in a row makes that row NaN, and
+ * so does a sum that leaves fp32: that of the row's squared differences to its mean (1.8e19 / sqrt(d) each
+ * are enough), or that of its values (3.4e38 / d; rows in registers are summed by warps and bear more).  Such a
+ * row's dX is NaN too, and with it dweight.  Nothing but X is needed for the backward pass.
  */
 lce_status_t lce_layer_norm_forward(const void* X, int64_t ldx, const void* weight, const void* bias,
                                     int64_t N, int64_t d, float eps, lce_dtype_t dtype, void* Y,

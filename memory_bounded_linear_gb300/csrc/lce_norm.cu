@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const NormArgs a)
     sum_over<1024, 4>(q, sh, turn4);
     const float off = q[0] * inv_d;
     float r = 1.f / sqrtf(fmaxf(fmaf(-off, off, q[1] * inv_d), 0.f) + a.eps);
-    if (!(fabsf(q[0]) < INFINITY)) r = NAN;  // fmaxf above drops a NaN
+    if (!(q[1] < INFINITY)) r = NAN;  // as inverse_deviation(): fmaxf above drops a NaN, and 1 / inf would be 0
     if constexpr (STATS) {
       // x^ = (x - mean - off) r keeps its bits only with both differences taken in turn
       if (threadIdx.x == 0) {

@@ -451,9 +451,10 @@ __device__ __forceinline__ uint64_t floor_of(float min_p, uint64_t largest) {
 __device__ __forceinline__ uint64_t mass_of(float top_p, uint64_t total) {
   return top_p > 0.f ? max(share_of(top_p, total, true), uint64_t(1)) : 1;
 }
-// The difference to the maximum up to which a token may have the weight `least`, and a little more.
+// The difference to the maximum up to which a token may have the weight `least`, and a little more.  The lowest bit of
+// a weight is always set, so that an odd one begins a unit below itself; 1 reaches as far as there are weights.
 __device__ __forceinline__ float reach_of(uint64_t least, const Scale& s) {
-  const float t = static_cast<float>(WEIGHT_BITS) - __log2f(static_cast<float>(least)) + 0.01f;
+  const float t = static_cast<float>(WEIGHT_BITS) - __log2f(static_cast<float>(least - 1)) + 0.01f;
   return fminf(s.d_max, t * 256.f * ptx::rcp_approx(s.c_hi));
 }
 // A logit below which all differences to the maximum are larger than d.

@@ -84,15 +84,27 @@ class TokenModel(torch.nn.Module):
         return lce.linear_cross_entropy(h.reshape(-1, h.shape[-1]), self.table, labels.reshape(-1))
 
     @torch.no_grad()
-    def next_tokens(self, tokens, **sampling):
+    def head(self):
+        """The table as linear_act's weight, whose rows come in eights: behind an odd vocabulary's there are zeros."""
+        more = -self.table.shape[0] % 8
+        return torch.nn.functional.pad(self.table, (0, 0, 0, more)) if more else self.table
+
+    @torch.no_grad()
+    def logits(self, tokens, head=None):
+        """Logits after each of tokens [n]; ``head`` is self.head(), where there is one already."""
+        head = self.head() if head is None else head
+        return lce.linear_act(self.hidden(tokens), head)[..., :self.table.shape[0]]
+
+    @torch.no_grad()
+    def next_tokens(self, tokens, head=None, **sampling):
         """A token after each of tokens [n]."""
-        return lce.sample_tokens(lce.linear_act(self.hidden(tokens), self.table), **sampling)
+        return lce.sample_tokens(self.logits(tokens, head), **sampling)
 
     @torch.no_grad()
     def generate(self, tokens, steps, **sampling):
-        out = [tokens]
+        out, head = [tokens], self.head()
         for _ in range(steps):
-            out.append(self.next_tokens(out[-1], **sampling))
+            out.append(self.next_tokens(out[-1], head, **sampling))
         return torch.stack(out, -1)
 
 

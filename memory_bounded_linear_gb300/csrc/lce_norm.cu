@@ -36,7 +36,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
 constexpr int64_t kMaxWidth = int64_t(1) << 30;  // columns are counted in 32 bits, a step past the end too
 constexpr int64_t kMaxElements = int64_t(1) << 48;
 
-// Partial sums of dw and db, blocks of the backward pass, at most.
+// Partial sums of dw and db, blocks of the backward pass, at most: a bound for the workspace, whatever the device.
 int64_t max_parts(int64_t N, int64_t d) {
   return std::min<int64_t>(std::max<int64_t>(N, 1), d > 1024 ? 152 * 4 : 152 * 8);
 }
@@ -604,7 +604,7 @@ constexpr int kForwardVectors = 2048, kBackwardVectors = 2048;
 // an SM of a device holds, once the kernel may use its shared memory there.
 template <typename K>
 cudaError_t launch_rows(K kernel, int64_t blocks, int threads, size_t smem, PerDevice<kMaxDevices>& resident, int* grid,
-                        int64_t most, cudaStream_t s, const NormArgs& a) {
+                        int64_t most, int num_sms, cudaStream_t s, const NormArgs& a) {
   int dev = 0, n = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -615,7 +615,7 @@ cudaError_t launch_rows(K kernel, int64_t blocks, int threads, size_t smem, PerD
                               : cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel, threads, smem);
   }, &n);
   if (e != cudaSuccess) return e;
-  *grid = static_cast<int>(std::min<int64_t>({blocks, int64_t(152) * n, most}));
+  *grid = static_cast<int>(std::min<int64_t>({blocks, int64_t(num_sms) * n, most}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(*grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -627,88 +627,88 @@ cudaError_t launch_rows(K kernel, int64_t blocks, int threads, size_t smem, PerD
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 template <typename E, int V, int T, int NV, bool FULL = false>
-cudaError_t forward_rows(const NormArgs& a, cudaStream_t s) {
+cudaError_t forward_rows(const NormArgs& a, int num_sms, cudaStream_t s) {
   if constexpr (V > 1 && !FULL) {
-    if (a.d == T * NV * V) return forward_rows<E, V, T, NV, true>(a, s);
+    if (a.d == T * NV * V) return forward_rows<E, V, T, NV, true>(a, num_sms, s);
   }
   static PerDevice<kMaxDevices> resident;
   constexpr int ROWS = kBlock<T> / T;
   int grid;
   return launch_rows(layer_norm_kernel<E, V, T, NV, FULL>, (a.N + ROWS - 1) / ROWS, kBlock<T>,
-                     Ahead<E, V, T, NV, 1, FULL>::BYTES, resident, &grid, a.N, s, a);
+                     Ahead<E, V, T, NV, 1, FULL>::BYTES, resident, &grid, a.N, num_sms, s, a);
 }
 template <typename E, int V>
 cudaError_t forward(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int64_t nv = (a.d + V - 1) / V;
   if constexpr (V < kVec<E>) {  // narrow vectors, more of them a thread
     constexpr int NV = Raw<E, V>::BYTES == 4 ? 8 : 16;
-    if (nv <= 32 * NV) return forward_rows<E, V, 32, NV>(a, s);
-    if (nv <= 64 * NV) return forward_rows<E, V, 64, NV>(a, s);
-    if (nv <= 128 * NV) return forward_rows<E, V, 128, NV>(a, s);
-    if (nv <= 256 * NV) return forward_rows<E, V, 256, NV>(a, s);
-    if (nv <= 512 * NV) return forward_rows<E, V, 512, NV>(a, s);
+    if (nv <= 32 * NV) return forward_rows<E, V, 32, NV>(a, num_sms, s);
+    if (nv <= 64 * NV) return forward_rows<E, V, 64, NV>(a, num_sms, s);
+    if (nv <= 128 * NV) return forward_rows<E, V, 128, NV>(a, num_sms, s);
+    if (nv <= 256 * NV) return forward_rows<E, V, 256, NV>(a, num_sms, s);
+    if (nv <= 512 * NV) return forward_rows<E, V, 512, NV>(a, num_sms, s);
   } else {
-  if (nv <= 32) return forward_rows<E, V, 32, 1>(a, s);
-  if (nv <= 64) return forward_rows<E, V, 32, 2>(a, s);
-  if (nv <= 128) return forward_rows<E, V, 32, 4>(a, s);
-  if (nv <= 256) return forward_rows<E, V, 64, 4>(a, s);
-  if (nv <= 512) return forward_rows<E, V, 128, 4>(a, s);
-  if (nv <= 768) return forward_rows<E, V, 192, 4>(a, s);
-  if (nv <= 1024) return forward_rows<E, V, 256, 4>(a, s);
-  if (nv <= kForwardVectors) return forward_rows<E, V, 512, 4>(a, s);
+  if (nv <= 32) return forward_rows<E, V, 32, 1>(a, num_sms, s);
+  if (nv <= 64) return forward_rows<E, V, 32, 2>(a, num_sms, s);
+  if (nv <= 128) return forward_rows<E, V, 32, 4>(a, num_sms, s);
+  if (nv <= 256) return forward_rows<E, V, 64, 4>(a, num_sms, s);
+  if (nv <= 512) return forward_rows<E, V, 128, 4>(a, num_sms, s);
+  if (nv <= 768) return forward_rows<E, V, 192, 4>(a, num_sms, s);
+  if (nv <= 1024) return forward_rows<E, V, 256, 4>(a, num_sms, s);
+  if (nv <= kForwardVectors) return forward_rows<E, V, 512, 4>(a, num_sms, s);
   }
   const int grid = static_cast<int>(std::min<int64_t>(a.N, 2 * num_sms));
   return launch_kernel(layer_norm_wide_kernel<E, V, false>, dim3(grid), 1024, s, a);
 }
 
-int64_t wide_chunks(int64_t N, int64_t d) {
+int64_t wide_chunks(int64_t N, int64_t d, int num_sms) {
   const int64_t tiles = (d + 2047) / 2048;
-  return std::max<int64_t>(1, std::min<int64_t>({N, (152 * 8 + tiles - 1) / tiles, max_parts(N, d)}));
+  return std::max<int64_t>(1, std::min<int64_t>({N, (int64_t(num_sms) * 8 + tiles - 1) / tiles, max_parts(N, d)}));
 }
 
 template <typename E, int V, int T, int NV, bool FULL = false>
-cudaError_t backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
+cudaError_t backward_rows(const NormArgs& a, int* parts, int num_sms, cudaStream_t s) {
   if constexpr (V > 1 && !FULL) {
-    if (a.d == T * NV * V) return backward_rows<E, V, T, NV, true>(a, parts, s);
+    if (a.d == T * NV * V) return backward_rows<E, V, T, NV, true>(a, parts, num_sms, s);
   }
   static PerDevice<kMaxDevices> resident[2];
   constexpr int ROWS = kBlock<T> / T;
   const int64_t blocks = (a.N + ROWS - 1) / ROWS;
   // two blocks an SM while a block has no more than four rows: partial sums are written and read once more
-  const int64_t most = a.part ? std::min(max_parts(a.N, a.d), std::max<int64_t>(2 * 152, a.N / 4)) : a.N;
+  const int64_t most = a.part ? std::min(max_parts(a.N, a.d), std::max<int64_t>(2 * num_sms, a.N / 4)) : a.N;
   // where a block has several rows, their sums meet in the same memory
   const size_t meet = ROWS > 1 ? 2 * sizeof(float) * NV * V * T : 0;
   const size_t bytes = std::max(Ahead<E, V, T, NV, 2, FULL>::BYTES, meet);
   if (a.part)
-    return launch_rows(layer_norm_grad_kernel<E, V, T, NV, FULL, true>, blocks, kBlock<T>, bytes, resident[1], parts, most, s, a);
-  return launch_rows(layer_norm_grad_kernel<E, V, T, NV, FULL, false>, blocks, kBlock<T>, bytes, resident[0], parts, most, s, a);
+    return launch_rows(layer_norm_grad_kernel<E, V, T, NV, FULL, true>, blocks, kBlock<T>, bytes, resident[1], parts, most, num_sms, s, a);
+  return launch_rows(layer_norm_grad_kernel<E, V, T, NV, FULL, false>, blocks, kBlock<T>, bytes, resident[0], parts, most, num_sms, s, a);
 }
 template <typename E, int V>
 cudaError_t backward(const NormArgs& a, int* parts, int num_sms, cudaStream_t s) {
   const int64_t nv = (a.d + V - 1) / V;
   if constexpr (V < kVec<E>) {
     constexpr int NV = Raw<E, V>::BYTES == 4 ? 8 : 16;
-    if (nv <= 32 * NV) return backward_rows<E, V, 32, NV>(a, parts, s);
-    if (nv <= 64 * NV) return backward_rows<E, V, 64, NV>(a, parts, s);
-    if (nv <= 128 * NV) return backward_rows<E, V, 128, NV>(a, parts, s);
-    if (nv <= 256 * NV) return backward_rows<E, V, 256, NV>(a, parts, s);
-    if (nv <= 512 * NV) return backward_rows<E, V, 512, NV>(a, parts, s);
-    if (NV < 16 && nv <= 512 * 16) return backward_rows<E, V, 512, 16>(a, parts, s);
+    if (nv <= 32 * NV) return backward_rows<E, V, 32, NV>(a, parts, num_sms, s);
+    if (nv <= 64 * NV) return backward_rows<E, V, 64, NV>(a, parts, num_sms, s);
+    if (nv <= 128 * NV) return backward_rows<E, V, 128, NV>(a, parts, num_sms, s);
+    if (nv <= 256 * NV) return backward_rows<E, V, 256, NV>(a, parts, num_sms, s);
+    if (nv <= 512 * NV) return backward_rows<E, V, 512, NV>(a, parts, num_sms, s);
+    if (NV < 16 && nv <= 512 * 16) return backward_rows<E, V, 512, 16>(a, parts, num_sms, s);
   } else {
-  if (nv <= 32) return backward_rows<E, V, 32, 1>(a, parts, s);
-  if (nv <= 64) return backward_rows<E, V, 32, 2>(a, parts, s);
-  if (nv <= 128) return backward_rows<E, V, 32, 4>(a, parts, s);
-  if (nv <= 256) return backward_rows<E, V, 64, 4>(a, parts, s);
-  if (nv <= 512) return backward_rows<E, V, 64, 8>(a, parts, s);
-  if (nv <= 768) return backward_rows<E, V, 128, 6>(a, parts, s);
-  if (nv <= 1024) return backward_rows<E, V, 128, 8>(a, parts, s);
-  if (nv <= kBackwardVectors) return backward_rows<E, V, 256, 8>(a, parts, s);
+  if (nv <= 32) return backward_rows<E, V, 32, 1>(a, parts, num_sms, s);
+  if (nv <= 64) return backward_rows<E, V, 32, 2>(a, parts, num_sms, s);
+  if (nv <= 128) return backward_rows<E, V, 32, 4>(a, parts, num_sms, s);
+  if (nv <= 256) return backward_rows<E, V, 64, 4>(a, parts, num_sms, s);
+  if (nv <= 512) return backward_rows<E, V, 64, 8>(a, parts, num_sms, s);
+  if (nv <= 768) return backward_rows<E, V, 128, 6>(a, parts, num_sms, s);
+  if (nv <= 1024) return backward_rows<E, V, 128, 8>(a, parts, num_sms, s);
+  if (nv <= kBackwardVectors) return backward_rows<E, V, 256, 8>(a, parts, num_sms, s);
   }
   const int grid = static_cast<int>(std::min<int64_t>(a.N, 2 * num_sms));
   cudaError_t e = launch_kernel(layer_norm_wide_kernel<E, V, true>, dim3(grid), 1024, s, a);
   if (e != cudaSuccess) return e;
   ++g_extra_kernels;
-  *parts = static_cast<int>(wide_chunks(a.N, a.d));
+  *parts = static_cast<int>(wide_chunks(a.N, a.d, num_sms));
   const unsigned tiles = static_cast<unsigned>((nv + 255) / 256);
   return launch_kernel(layer_norm_wide_grad_kernel<E, V>, dim3(tiles, *parts), 256, s, a);
 }

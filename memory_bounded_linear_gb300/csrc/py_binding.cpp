@@ -341,7 +341,7 @@ PyObject* clip(PyObject* const* a) {
 // The bytes that a matrix of rows takes.
 struct Span {
   uintptr_t begin, end;
-  size_t stride, width;  // bytes of a row's step and of a row
+  size_t rows, stride, width;  // bytes of a row's step and of a row
 };
 Span span_of(const at::Tensor& t) {
   const size_t e = t.element_size();
@@ -349,17 +349,18 @@ Span span_of(const at::Tensor& t) {
   const size_t n = t.dim() == 2 ? t.size(0) : 1;
   const size_t stride = t.dim() == 2 && n > 1 ? t.stride(0) * e : width;
   const uintptr_t b = reinterpret_cast<uintptr_t>(t.data_ptr());
-  return Span{b, t.numel() ? b + (n - 1) * stride + width : b, stride, width};
+  return Span{b, t.numel() ? b + (n - 1) * stride + width : b, n, stride, width};
 }
 // Refuses an output that shares elements with another array of the call.  Column ranges of one wider array
-// do not.
+// do not, nor does a single row between the rows of one.
 void apart(const at::Tensor& out, const char* name, const at::Tensor& in, const char* other) {
   if (!in.defined()) return;
   const Span a = span_of(out), b = span_of(in);
   if (a.begin >= b.end || b.begin >= a.end) return;
-  if (a.stride == b.stride && a.stride > 0) {
-    const size_t off = (b.begin >= a.begin ? b.begin - a.begin : a.stride - (a.begin - b.begin) % a.stride) % a.stride;
-    if (off >= a.width && off + b.width <= a.stride) return;
+  const size_t stride = a.rows == 1 ? b.stride : b.rows == 1 || a.stride == b.stride ? a.stride : 0;
+  if (stride > 0) {
+    const size_t off = (b.begin >= a.begin ? b.begin - a.begin : stride - (a.begin - b.begin) % stride) % stride;
+    if (off >= a.width && off + b.width <= stride) return;
   }
   refuse(PyExc_ValueError, name, " shares memory with ", other);
 }

@@ -358,7 +358,7 @@ lce_status_t lce_clip_grad_norm(const void* const* grads, void* const* out, cons
  *     and statistics are fp32 or wider, each result is rounded once.
  *   - Widths are any number >= 1, and pointers need the alignment of an element only (tokens 8 bytes,
  *     the workspace 16).  Rows whose width, stride and address are multiples of 16 bytes are moved 16
- *     bytes at a time, others an element at a time.
+ *     bytes at a time, others 4 bytes at a time where they are multiples of that, else an element at a time.
  *   - X, dY, Y and logits have row strides (elements) at least their width; all else is dense.  Outputs do not
  *     overlap inputs, except Y == X with equal strides in lce_layer_norm_forward.
  *   - Shape rules (LCE_ERR_UNSUPPORTED_SHAPE otherwise): row counts >= 0 (0: nothing is written but
@@ -450,8 +450,9 @@ typedef struct {
  * probability that the token was drawn with (0 at temperature 0).
  * A logit of -inf is never drawn; among logits of +inf all are equally likely.  A row with a NaN, or
  * without a logit above -inf, gives the token -1 and a NaN logprob.
- * Weights are integers of about 2^-39 of the largest, with a relative error of about 2^-32; their sums are
- * exact, so that the result depends on nothing but the arguments.  V is at most 2^22.
+ * Weights are odd integers, in units of about 2^-39 of the largest: off by up to a unit, beside a relative error
+ * of about 2^-32; below 2^-40 of the largest they are 0.  Their sums are exact, so that the result depends on
+ * nothing but the arguments.  V is at most 2^22.
  */
 lce_status_t lce_sample(const void* logits, int64_t ld, int64_t B, int64_t V, lce_dtype_t dtype,
                         const float* uniform, const lce_sampling_t* settings, int64_t* tokens,

@@ -18,8 +18,9 @@
 // most; a bitmap of the tokens and zeros beside the sums wrote each once, but left the sort's 25 us bare.
 //
 // Inside a captured graph: lookup of 32768 x 6144 bf16 79 us (frequent rows come from L2: the 403 MB written alone
-// would take 59), 48 x 6144 2.0 us.  Gradient of 32768 x 2048, 151,936 tokens, bf16, Zipf(1.1): 124 us, 0.90 of the copy
-// rate over dy and dE; 1999 x 515 fp32, 8,191 tokens 13.8 us (three launches in a row, 3 us of bytes).
+// would take 59), 48 x 6144 2.0 us.  Gradient of 32768 x 2048, 151,936 tokens, bf16, Zipf(1.1): 125 us, 0.89 of the copy
+// rate over dy and dE; 1999 x 515 fp32, 8,191 tokens 13.8 us (three launches in a row, 3 us of bytes).  Where a smaller table
+// leaves the sort bare: 16384 x 512 of 20,000 tokens 31 us (5.5 of bytes), 131072 x 1024 of 50,000 105 (55).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -11,10 +11,12 @@
 // The backward pass recomputes both statistics from x, which it reads anyway: the forward pass keeps nothing.  Its
 // blocks hold the columns' partial sums of dw and db in registers over all their rows and write them once; a
 // second launch adds them in a fixed order (2 to 4 us).
-// Inside a captured graph, bf16: forward 32768 x 6144 127 us (0.93 of the copy rate), 16384 x 4096 45 (0.88);
-// backward 32768 x 6144 199 (0.90), 16384 x 4096 68 (0.87), 16384 x 2048 40 (0.73); forward of one row 2.0.  At
+// Inside a captured graph, bf16: forward 32768 x 6144 128 us (0.92 of the copy rate), 16384 x 4096 46 (0.86);
+// backward 32768 x 6144 199 (0.89), 16384 x 4096 70 (0.85), 16384 x 2048 41 (0.73); forward of one row 2.0.  At
 // 16384 x 4096 backward with 64 / 128 / 256 / 512 threads a row: 68 / 75 / 100 / 204 us; forward with 64 / 128 / 256:
-// 55 / 45 / 62.
+// 55 / 45 / 62.  Rows that fill no class run masked: 16384 x 7168 92 and 149 us (0.75, 0.70).
+// Farther from their floor: 16384 x 2046 bf16 by 4 bytes 37 and 60 us (0.53, 0.49), 16384 x 2047 by single elements 54 and
+// 84 (0.36); rows that are read again, 2048 x 20000 70 and 137 (0.35, 0.26).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -597,7 +599,8 @@ bool stride_ok(int64_t ld, int64_t d, int64_t N) {
   return ld >= d && ld <= kMaxElements && (N <= 1 || ld <= (int64_t(1) << 62) / N);
 }
 
-// Widest row of the register kernels, in vectors.
+// Widest row of the register kernels, in vectors of 16 bytes: 16,384 bf16 or 8,192 fp32.  Of narrow vectors: 8,192 bf16
+// either way, and by words of 4 bytes 8,192 bf16 or 4,096 fp32 forward, twice that backward.
 constexpr int kForwardVectors = 2048, kBackwardVectors = 2048;
 
 // A dependent launch of one of the kernels above on as many blocks as the SMs hold at once; `resident` keeps how many
@@ -637,6 +640,10 @@ cudaError_t forward_rows(const NormArgs& a, int num_sms, cudaStream_t s) {
   return launch_rows(layer_norm_kernel<E, V, T, NV, FULL>, (a.N + ROWS - 1) / ROWS, kBlock<T>,
                      Ahead<E, V, T, NV, 1, FULL>::BYTES, resident, &grid, a.N, num_sms, s, a);
 }
+// Classes of rows by their vectors, each twice the one before: what a class does not fill is masked, and a row that fills
+// it asks for nothing.  Between 512 and 1,024 there is one more, of 768 (no others were tried): us with it / without, bf16,
+// forward of 32768 rows and backward of 16384: 4104 wide 136 / 149 and 120 / 127, 4608 136 / 151 and 111 / 118,
+// 5120 142 / 155 and 115 / 121, 5632 152 / 162 and 126 / 132, 6144 129 / 168 and 107 / 135.
 template <typename E, int V>
 cudaError_t forward(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int64_t nv = (a.d + V - 1) / V;

@@ -22,14 +22,17 @@
 // many more bits than fp32 has, and must not depend on the order of additions.  Weights are integers of 2^-39:
 // z log2(e) / temperature as a product with a constant of two floats, cut at an integer k of 256ths, whose difference
 // to the product takes one rounding; a table of 2^(j/256) in two floats and a cubic for the rest, |rest| <= 1/2 of
-// 256ths; relative error 2^-31.7 at most, 2^-34 as a rule.  Sums of integers are exact in any order, also by atomics.
+// 256ths; relative error 2^-31.7 at most, 2^-34 as a rule, and up to a unit for the bits below it.  Sums of integers are
+// exact in any order, also by atomics.
 // Double precision exponentials would cost ten times as much here (two operations a cycle and SM); with errors of 2^-23
 // about one row in some thousand would draw another token.
 //
-// Bound by instructions (25 for a weight, 6 for a bin) and by the latency of a row's dozen steps, which show as
-// waits at barriers and as first executions of code: issue slots are 40% busy.  Inside a captured graph: 1 x 151,936 bf16
-// greedy 4.4 us, top-k 50 and top-p 0.95 12, all tokens 11, top-p 0.9 25; 64 x 151,936 fp32 greedy 14, all 33,
-// top-p 0.9 72; 128 x 200,000 bf16 min-p 0.05 30 to 54, top-p 0.9 98 (by bins and lists 208).
+// Bound by latency: a row takes a dozen short steps, one after the other, which show as waits at barriers and as first
+// executions of code, and where a row is not staged by reading L2 again in each.  Issue slots are 39 to 44% busy (25
+// instructions for a weight, 6 for a bin; 125 a logit over all steps of top-p of fp32), so that instructions alone bound
+// nothing.  Inside a captured graph over logits that are not in L2: 1 x 151,936 bf16 greedy 4.1 us, top-k 50 and top-p 0.95 12, all
+// tokens 11, top-p 0.9 24; 64 x 151,936 fp32 greedy 17, all 37, top-p 0.9 78; 128 x 200,000 bf16 min-p 0.05 36 to 40, top-p
+// 0.9 106 (by bins and lists 208).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
